@@ -97,7 +97,15 @@ typedef enum {
   MOE_ERR_DEVICE = 4       /* moe_device_error only: a kernel recorded a device-side fault */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP4 = 2, MOE_MXFP4_A8 = 3, MOE_MXFP4_A4 = 4 } moe_dtype;
+/* MOE_F16 is a type of the operators in moe_ops.h; the layer does not take it. */
+typedef enum {
+  MOE_F32 = 0,
+  MOE_BF16 = 1,
+  MOE_MXFP4 = 2,
+  MOE_MXFP4_A8 = 3,
+  MOE_MXFP4_A4 = 4,
+  MOE_F16 = 5
+} moe_dtype;
 
 /* Layer shape and numerics.  K3 values: H=7168, L=3584, E=896, k=16, I=3072,
  * S=2, Is=3072 (dimension table of the page cited above). */

@@ -31,7 +31,7 @@ def up_to_date() -> bool:
     if not os.path.exists(LIB):
         return False
     t = os.path.getmtime(LIB)
-    deps = sources() + [os.path.join(HERE, "..", "include", "moe.h"), __file__]
+    deps = sources() + [os.path.join(HERE, "..", "include", h) for h in ("moe.h", "moe_ops.h")] + [__file__]
     return all(os.path.getmtime(s) <= t for s in deps if os.path.exists(s))
 
 

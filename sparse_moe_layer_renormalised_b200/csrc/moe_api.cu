@@ -1769,3 +1769,6 @@ extern "C" moe_status moe_qb_bias_update(const moe_dims* d, const float* scores,
   qb_quantile_kernel<<<E, 32, 0, s>>>(hist, E, nbins, c, lo, w, bias_in, bias_out, quantile_out);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
+
+// The operators around the layer (include/moe_ops.h).
+#include "ops_api.cuh"
