@@ -7,6 +7,8 @@
  *                                     sigmoid scores, selection bias, groups of
  *                                     experts, masked experts
  *   moe_norm, moe_norm_backward       layer norm and RMS norm of rows
+ *   moe_linear, moe_linear_backward   matrix product with bias, activation and
+ *                                     residual in its epilogue
  *   moe_clip_grads                    global norm of many gradient tensors, and
  *                                     clipping
  *
@@ -111,6 +113,49 @@ MOE_API size_t moe_norm_backward_workspace_size(const moe_norm_desc* d);
 MOE_API moe_status moe_norm_backward(const moe_norm_desc* d, const void* dy, const void* x, const float* gamma,
                                      const float* mean, const float* rstd, void* dx, float* dgamma, float* dbeta,
                                      void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- linear */
+
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,      /* a * sigmoid(a) */
+  MOE_ACT_GELU = 3,      /* a * (1 + erf(a / sqrt 2)) / 2 */
+  MOE_ACT_GELU_TANH = 4  /* a * (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2 */
+} moe_act;
+
+typedef struct {
+  int64_t M;       /* rows of x, 0 <= M <= 2^31 - 1 */
+  int32_t N;       /* rows of the weight: columns of y; a multiple of 8 */
+  int32_t K;       /* columns of x and of the weight; a multiple of 8 */
+  moe_act act;
+  moe_dtype dtype; /* x, weight and, in the backward pass, all matrices: MOE_BF16 or MOE_F16 */
+  moe_dtype y_out; /* y and the residual: equal to dtype, or MOE_F32 */
+} moe_linear_desc;
+
+/* y = act(x[M, K] . W[N, K]^T + bias) + residual, on the tensor cores with fp32
+ * accumulation; bias, activation and residual are applied to the fp32
+ * accumulator and y is rounded once.  bias [N] fp32, residual [M, N] in the type
+ * of y, each NULL for none; pre [M, N] in `dtype` receives x W^T + bias for the
+ * backward pass, or is NULL.  y may be the residual.  N or K not a multiple of 8
+ * is MOE_ERR_UNSUPPORTED, as is MOE_F32 for `dtype`.
+ * Workspace: moe_linear_workspace_size(d) bytes (may be 0: ws may be NULL then). */
+MOE_API size_t moe_linear_workspace_size(const moe_linear_desc* d);
+MOE_API moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* weight, const float* bias,
+                              const void* residual, void* pre, void* y, void* ws, size_t ws_bytes,
+                              moe_stream_t stream);
+
+/* With dp = dy act'(pre) (pre from moe_linear; NULL for MOE_ACT_NONE):
+ *   dx = dp . W [M, K],  dweight = dp^T . x [N, K],  dbias = sum_m dp [N] fp32
+ * dp is rounded once to `dtype` as the products' operand; dbias is summed from the
+ * unrounded fp32 dp in a fixed order.  dx, dweight and dbias may each be NULL; dx
+ * and dweight are in `dtype`, dy [M, N] in `dtype`.  relu'(0) = 0.  The residual's
+ * gradient is dy itself.  M = 0 writes zeros to dweight and dbias.
+ * Workspace: moe_linear_backward_workspace_size(d) bytes (0 for a bad descriptor). */
+MOE_API size_t moe_linear_backward_workspace_size(const moe_linear_desc* d);
+MOE_API moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, const void* pre, const void* x,
+                                       const void* weight, void* dx, void* dweight, float* dbias, void* ws,
+                                       size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- clipping */
 

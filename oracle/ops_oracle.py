@@ -118,6 +118,38 @@ def norm_backward(dy, x, gamma, mean, rstd, kind="layer"):
     return dx * r, (dy * xh).sum(0), dy.sum(0)
 
 
+# ------------------------------------------------------------------------------ linear
+def act(a, kind):
+    if kind == "relu":
+        return torch.where(a > 0, a, torch.zeros_like(a))
+    if kind == "silu":
+        return a / (1.0 + torch.exp(-a))
+    if kind == "gelu":
+        return 0.5 * a * (1.0 + torch.erf(a / math.sqrt(2.0)))
+    if kind == "gelu_tanh":
+        return 0.5 * a * (1.0 + torch.tanh(math.sqrt(2.0 / math.pi) * (a + 0.044715 * a ** 3)))
+    return a
+
+
+def act_grad(a, kind):
+    a = a.to(F64).detach().requires_grad_(True)
+    return torch.autograd.grad(act(a, kind).sum(), a)[0]
+
+
+def linear(x, weight, bias, residual, kind):
+    """(pre, y)"""
+    pre = x.to(F64) @ weight.to(F64).T
+    pre = pre if bias is None else pre + bias.to(F64)
+    y = act(pre, kind)
+    return pre, (y if residual is None else y + residual.to(F64))
+
+
+def linear_backward(dy, pre, x, weight, kind):
+    """(dp, dx, dweight, dbias), dp unrounded"""
+    dp = dy.to(F64) if kind == "none" else dy.to(F64) * act_grad(pre, kind)
+    return dp, dp @ weight.to(F64), dp.T @ x.to(F64), dp.sum(0)
+
+
 # ------------------------------------------------------------------------------ clipping
 def clip(grads, max_norm, kind="l2"):
     """(norm, [g * factor])"""

@@ -1,10 +1,11 @@
 """ctypes binding of include/moe_ops.h, the operators around the layer: routing
-from logits, layer and RMS norm, gradient clipping.
+from logits, layer and RMS norm, the dense product with an epilogue, gradient
+clipping.
 
 As in _binding: argument marshalling only, every function forwards to the
 library's function of the same name and returns its moe_status; tensors may be
-torch tensors, raw addresses or None.  The descriptors (route_desc, norm_desc)
-are plain C structs that a caller makes once per shape and passes
+torch tensors, raw addresses or None.  The descriptors (route_desc, norm_desc,
+linear_desc) are plain C structs that a caller makes once per shape and passes
 to every call.
 """
 from __future__ import annotations
@@ -17,11 +18,14 @@ from ._binding import _nbytes, _ptr, _stream
 MOE_F16 = 5
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
 MOE_CLIP_L2, MOE_CLIP_MAX = 0, 1
 
 _DTYPES = {"f32": _b.MOE_F32, "bf16": _b.MOE_BF16, "f16": MOE_F16}
 _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 _NORMS = {"layer": MOE_NORM_LAYER, "rms": MOE_NORM_RMS}
+_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU,
+         "gelu_tanh": MOE_ACT_GELU_TANH}
 _CLIPS = {"l2": MOE_CLIP_L2, "max": MOE_CLIP_MAX}
 
 EXPORTED_OPS = (
@@ -30,6 +34,10 @@ EXPORTED_OPS = (
     "moe_norm",
     "moe_norm_backward_workspace_size",
     "moe_norm_backward",
+    "moe_linear_workspace_size",
+    "moe_linear",
+    "moe_linear_backward_workspace_size",
+    "moe_linear_backward",
     "moe_clip_grads_workspace_size",
     "moe_clip_grads",
 )
@@ -44,6 +52,11 @@ class moe_route_desc(ctypes.Structure):
 class moe_norm_desc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("kind", ctypes.c_int), ("eps", ctypes.c_float),
                 ("dtype", ctypes.c_int)]
+
+
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("act", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("y_out", ctypes.c_int)]
 
 
 class moe_grad_tensor(ctypes.Structure):
@@ -61,12 +74,16 @@ def _lib() -> ctypes.CDLL:
     if _ready is not L:
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         pr, pn = ctypes.POINTER(moe_route_desc), ctypes.POINTER(moe_norm_desc)
-        pg = ctypes.POINTER(moe_grad_tensor)
+        pl, pg = ctypes.POINTER(moe_linear_desc), ctypes.POINTER(moe_grad_tensor)
         L.moe_route.argtypes = [pr, vp, vp, vp, vp, vp]
         L.moe_route_backward.argtypes = [pr, vp, vp, vp, vp, vp]
         L.moe_norm.argtypes = [pn] + [vp] * 7
         L.moe_norm_backward_workspace_size.argtypes = [pn]
         L.moe_norm_backward.argtypes = [pn] + [vp] * 9 + [sz, vp]
+        L.moe_linear_workspace_size.argtypes = [pl]
+        L.moe_linear.argtypes = [pl] + [vp] * 7 + [sz, vp]
+        L.moe_linear_backward_workspace_size.argtypes = [pl]
+        L.moe_linear_backward.argtypes = [pl] + [vp] * 8 + [sz, vp]
         L.moe_clip_grads_workspace_size.argtypes = [pg, i32]
         L.moe_clip_grads.argtypes = [pg, i32, ctypes.c_int, ctypes.c_float, vp, vp, sz, vp]
         for f in EXPORTED_OPS:
@@ -83,6 +100,11 @@ def route_desc(T: int, E: int, k: int, groups: int = 1, keep_groups: int | None 
 
 def norm_desc(T: int, H: int, kind: str = "layer", eps: float = 1e-6, dtype: str = "bf16") -> moe_norm_desc:
     return moe_norm_desc(T, H, _NORMS[kind], eps, _DTYPES[dtype])
+
+
+def linear_desc(M: int, N: int, K: int, act: str = "none", dtype: str = "bf16",
+                y_out: str | None = None) -> moe_linear_desc:
+    return moe_linear_desc(M, N, K, _ACTS[act], _DTYPES[dtype], _DTYPES[dtype if y_out is None else y_out])
 
 
 def moe_route(d: moe_route_desc, logits, bias, idx, w, stream=None) -> int:
@@ -113,6 +135,25 @@ def moe_norm_backward(d: moe_norm_desc, dy, x, gamma, mean, rstd, dx, dgamma, db
                       stream=None) -> int:
     return _lib().moe_norm_backward(ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
                                     _ptr(dgamma), _ptr(dbeta), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
+
+
+def moe_linear_workspace_size(d: moe_linear_desc) -> int:
+    return int(_lib().moe_linear_workspace_size(ctypes.byref(d)))
+
+
+def moe_linear(d: moe_linear_desc, x, weight, bias, residual, pre, y, ws=None, ws_bytes=None, stream=None) -> int:
+    return _lib().moe_linear(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(pre), _ptr(y),
+                             _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
+
+
+def moe_linear_backward_workspace_size(d: moe_linear_desc) -> int:
+    return int(_lib().moe_linear_backward_workspace_size(ctypes.byref(d)))
+
+
+def moe_linear_backward(d: moe_linear_desc, dy, pre, x, weight, dx, dweight, dbias, ws, ws_bytes=None,
+                        stream=None) -> int:
+    return _lib().moe_linear_backward(ctypes.byref(d), _ptr(dy), _ptr(pre), _ptr(x), _ptr(weight), _ptr(dx),
+                                      _ptr(dweight), _ptr(dbias), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
 
 
 class GradList:

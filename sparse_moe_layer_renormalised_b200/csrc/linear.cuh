@@ -1,0 +1,608 @@
+// Dense products with an epilogue on the tensor cores, forward and backward:
+//
+//   out[q, p] = f( sum_r Q(q, r) * P(p, r) )        p contiguous in out
+//
+//   y  = act(x W^T + b) + res:  q = token, p = weight row,     r = feature
+//   dx = dp W:                  q = token, p = feature,        r = weight row
+//   dW = dp^T x:                q = weight row, p = feature,   r = token
+//
+// Each operand is either r-contiguous ("K-major": x, W and dp as they lie) or
+// contiguous along its own rows ("MN-major": W for dx, dp and x for dW); both
+// come by TMA with the 128-byte swizzle and need no transposed copy:
+//   K-major   boxes of 64 r x n rows; 8-row groups 1024 bytes apart
+//   MN-major  boxes of 64 rows x 64 r, 128 bytes a step of r; 64-row boxes 8192
+//             bytes apart
+// Tails of every dimension are the zeros that TMA fills in.
+//
+// linear_wide_kernel: CTA pairs (tcgen05.mma.cta_group::2, 256 x BN tiles, BN a
+// multiple of 32 up to 256), persistent, two accumulators in tensor memory so
+// that a tile's epilogue runs under the next one's products.  For large
+// products; bound by the tensor cores.
+//
+// linear_skinny_kernel: P on the MMA's 128-row side and at most 128 rows of Q
+// beside it, the sum over r split over the CTAs of a cluster, which add up each
+// other's partial sums through distributed shared memory in rank order.  For
+// few rows, where the read of P bounds the call and a 256-row tile would be
+// mostly padding, and for outputs too small to fill the machine.
+#pragma once
+
+#include "gemm_expert.cuh"
+#include "ops_common.cuh"
+
+namespace moe {
+
+constexpr int LIN_BK = 64;
+constexpr uint32_t LIN_BOX_MN = 64 * LIN_BK * 2;  // bytes of an MN-major box
+
+// Descriptor of an MN-major tile in the layout above.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(LIN_BOX_MN >> 4) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) |
+         (static_cast<uint64_t>(2u) << 61);
+}
+
+// Instruction descriptor of kind::f16 with fp32 accumulation: operand format
+// (0 f16, 1 bf16; the same for both), transpose bits 15 (A) and 16 (B) for
+// MN-major operands.
+__host__ __device__ constexpr uint32_t lin_idesc(int M, int N, bool bf16, bool a_mn, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+enum LinAct : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+// sigmoid by the fast exponential: relative error below 2^-23 (4 + 1.2 |a|).
+__device__ __forceinline__ float lin_sigmoid(float a) { return __fdividef(1.0f, 1.0f + __expf(fminf(-a, 80.f))); }
+
+constexpr float kSqrt2OverPi = 0.7978845608028654f;
+
+__device__ __forceinline__ float lin_act(float a, int act) {
+  switch (act) {
+    case kActRelu:
+      return a > 0.f ? a : (a == a ? 0.f : a);
+    case kActSilu:
+      return a * lin_sigmoid(a);
+    case kActGelu:
+      return 0.5f * a * (1.0f + erff(a * 0.7071067811865476f));
+    case kActGeluTanh:  // (1 + tanh u) / 2 = sigmoid(2 u)
+      return a * lin_sigmoid(2.f * kSqrt2OverPi * (a + 0.044715f * a * a * a));
+    default:
+      return a;
+  }
+}
+
+__device__ __forceinline__ float lin_act_grad(float a, int act) {
+  switch (act) {
+    case kActRelu:
+      return a > 0.f ? 1.f : 0.f;
+    case kActSilu: {
+      const float s = lin_sigmoid(a);
+      return s * (1.0f + a * (1.0f - s));
+    }
+    case kActGelu:
+      return 0.5f * (1.0f + erff(a * 0.7071067811865476f)) + a * 0.3989422804014327f * __expf(-0.5f * a * a);
+    case kActGeluTanh: {
+      const float s = lin_sigmoid(2.f * kSqrt2OverPi * (a + 0.044715f * a * a * a));
+      return s + a * 2.f * s * (1.f - s) * kSqrt2OverPi * (1.f + 3.f * 0.044715f * a * a);
+    }
+    default:
+      return 1.f;
+  }
+}
+
+struct LinMaps {
+  CUtensorMap p, q;
+};
+
+struct LinParams {
+  long long Q;
+  int P, nkb;       // contraction blocks of 64
+  int p_mn, q_mn;   // operand layouts
+  int bf16;         // operand type: bf16 or f16
+  int p_tiles, q_tiles, bn;  // wide: bn columns (P) a tile; skinny: bn rows (Q) a tile
+  const float* bias;         // [P] or null
+  const void* residual;      // [Q, P] in the type of out, or null
+  void* pre;                 // [Q, P] in the operand type, or null
+  void* out;
+  int act;
+  int fault_site;
+};
+
+// bias, pre, activation and residual of NC consecutive outputs of a row (NC a
+// multiple of 4; 16-bit types in 8-byte, or for NC = 32 in 16-byte accesses).
+template <typename OutT, int NC>
+__device__ __forceinline__ void lin_finish(const LinParams& p, long long q, int col, float* a) {
+  const long long at = q * p.P + col;
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < NC; i += 4) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col + i));
+      a[i] += b.x;
+      a[i + 1] += b.y;
+      a[i + 2] += b.z;
+      a[i + 3] += b.w;
+    }
+  }
+  if (p.pre != nullptr) {
+    uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.pre) + at);
+#pragma unroll
+    for (int i = 0; i < NC; i += 4)
+      d[i / 4] = p.bf16 ? make_uint2(op_pack(a[i], a[i + 1], __nv_bfloat16()), op_pack(a[i + 2], a[i + 3], __nv_bfloat16()))
+                        : make_uint2(op_pack(a[i], a[i + 1], __half()), op_pack(a[i + 2], a[i + 3], __half()));
+  }
+  if (p.act != kActNone) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) a[i] = lin_act(a[i], p.act);
+  }
+  OutT* out = static_cast<OutT*>(p.out) + at;
+  const OutT* res = static_cast<const OutT*>(p.residual) + at;
+  constexpr int W = sizeof(OutT) == 4 ? 4 : NC % 8 == 0 ? 8 : 4;  // outputs per access
+#pragma unroll
+  for (int i = 0; i < NC; i += W) {
+    if constexpr (sizeof(OutT) == 4) {
+      if (p.residual != nullptr) {
+        const float4 r = *reinterpret_cast<const float4*>(res + i);
+        a[i] += r.x;
+        a[i + 1] += r.y;
+        a[i + 2] += r.z;
+        a[i + 3] += r.w;
+      }
+      *reinterpret_cast<float4*>(out + i) = make_float4(a[i], a[i + 1], a[i + 2], a[i + 3]);
+    } else if constexpr (W == 8) {
+      if (p.residual != nullptr) {
+        float r[8];
+        op_unpack16<OutT>(*reinterpret_cast<const uint4*>(res + i), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[i + j] += r[j];
+      }
+      *reinterpret_cast<uint4*>(out + i) = op_pack16<OutT>(a + i);
+    } else {
+      if (p.residual != nullptr) {
+        const uint2 u = *reinterpret_cast<const uint2*>(res + i);
+        const float2 r0 = op_unpack(u.x, OutT()), r1 = op_unpack(u.y, OutT());
+        a[i] += r0.x;
+        a[i + 1] += r0.y;
+        a[i + 2] += r1.x;
+        a[i + 3] += r1.y;
+      }
+      *reinterpret_cast<uint2*>(out + i) = make_uint2(op_pack(a[i], a[i + 1], OutT()), op_pack(a[i + 2], a[i + 3], OutT()));
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ wide
+constexpr int LW_STAGES = 6;
+constexpr uint32_t LW_OPER_BYTES = 128 * LIN_BK * 2;  // one operand's stage in a CTA
+constexpr int LW_THREADS = 32 * 10;
+constexpr size_t LW_SMEM = 1024 + static_cast<size_t>(LW_STAGES) * 2 * LW_OPER_BYTES + 256;
+constexpr int LW_GROUP = 8;  // Q tiles that share a run of P tiles through L2
+
+struct LinTile {
+  int q, p;
+};
+
+// Tiles in groups of LW_GROUP rows of tiles, the P tile outside and the Q tile
+// inside a group: the pairs at work at one time share few operand rows.
+__device__ __forceinline__ LinTile lw_tile(int w, const LinParams& p) {
+  const int per = LW_GROUP * p.p_tiles;
+  const int grp = w / per, r = w - grp * per;
+  const int rows = min(LW_GROUP, p.q_tiles - grp * LW_GROUP);
+  const int pt = r / rows;
+  return {grp * LW_GROUP + (r - pt * rows), pt};
+}
+
+template <typename OutT>
+__global__ void __launch_bounds__(LW_THREADS, 1)
+    linear_wide_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
+  extern __shared__ uint8_t lw_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lw_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;                                // Q rows
+  uint8_t* sB = smem + LW_STAGES * LW_OPER_BYTES;    // P rows
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + LW_STAGES * LW_OPER_BYTES);
+  uint64_t* empty = full + LW_STAGES;
+  uint64_t* acc_full = empty + LW_STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int total = p.q_tiles * p.p_tiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < LW_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 16);  // the eight epilogue warps of both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&maps.p);
+    tma_prefetch_desc(&maps.q);
+  }
+  if (warp == 1) ex_tmem_alloc<2>(tmem_holder);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int half = p.bn >> 1;  // P rows that this CTA stages
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0u, issued_parity = 0u;
+      bool ok = true;
+      const int p_boxes = (half + 63) >> 6;
+      const uint32_t bytes = 2u * (LW_OPER_BYTES + (p.p_mn ? p_boxes * LIN_BOX_MN : static_cast<uint32_t>(half) * 128u));
+      for (int w = pair; w < total && ok; w += npairs) {
+        const LinTile t = lw_tile(w, p);
+        const int q0 = t.q * 256 + static_cast<int>(rank) * 128;
+        const int p0 = t.p * p.bn + static_cast<int>(rank) * half;
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort, p.fault_site + 1)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          const int kc = kb * LIN_BK;
+          uint8_t* a_dst = sA + stage * LW_OPER_BYTES;
+          uint8_t* b_dst = sB + stage * LW_OPER_BYTES;
+          if (p.q_mn) {
+            ex_tma_load<2>(a_dst, &maps.q, &full[stage], q0, kc);
+            ex_tma_load<2>(a_dst + LIN_BOX_MN, &maps.q, &full[stage], q0 + 64, kc);
+          } else {
+            ex_tma_load<2>(a_dst, &maps.q, &full[stage], kc, q0);
+          }
+          if (p.p_mn) {
+            for (int b = 0; b < p_boxes; ++b)
+              ex_tma_load<2>(b_dst + b * LIN_BOX_MN, &maps.p, &full[stage], p0 + b * 64, kc);
+          } else {
+            ex_tma_load<2>(b_dst, &maps.p, &full[stage], kc, p0);
+          }
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == LW_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // the even CTA's barriers count both CTAs' bytes: every load lands before
+      // the pair may exit
+      if (leader) {
+        volatile int never = 0;
+        for (int s = 0; s < LW_STAGES; ++s)
+          if ((issued >> s) & 1u) mbar_wait(&full[s], (issued_parity >> s) & 1u, &never, p.fault_site + 2);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer (even CTA)
+    if (lane == 0 && leader) {
+      const uint32_t idesc = lin_idesc(256, p.bn, p.bf16 != 0, p.q_mn != 0, p.p_mn != 0);
+      // an MMA takes 16 steps of r: 32 bytes of a K-major row, two 8-step groups of an MN-major tile
+      const uint32_t a_step = p.q_mn ? 2048u : 32u, b_step = p.p_mn ? 2048u : 32u;
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int w = pair; w < total && ok; w += npairs) {
+        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, abort, p.fault_site + 3)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          if (!mbar_wait(&full[stage], phase, abort, p.fault_site + 4)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(sA + stage * LW_OPER_BYTES);
+          const uint32_t b_addr = smem_u32(sB + stage * LW_OPER_BYTES);
+          const uint64_t ad = p.q_mn ? sw128_mnmajor_desc(a_addr) : sw128_kmajor_desc(a_addr);
+          const uint64_t bd = p.p_mn ? sw128_mnmajor_desc(b_addr) : sw128_kmajor_desc(b_addr);
+#pragma unroll
+          for (int kk = 0; kk < LIN_BK / 16; ++kk)
+            ex_mma<2>(d_tmem, ad + ((kk * a_step) >> 4), bd + ((kk * b_step) >> 4), idesc, (kb | kk) != 0 ? 1u : 0u);
+          ex_commit<2>(&empty[stage]);
+          if (++stage == LW_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ex_commit<2>(&acc_full[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      ex_commit<2>(drain);
+    }
+    // both CTAs: every MMA that touches this CTA's memory is done
+    if (lane == 0) {
+      volatile int never = 0;
+      mbar_wait(drain, 0u, &never, p.fault_site + 5);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    // two sets of four warps take alternate chunks of 32 columns
+    const int quarter = warp & 3;
+    const int set = warp >= 6 ? 1 : 0;
+    const uint32_t acc_empty_leader = map_to_rank(smem_u32(&acc_empty[0]), 0u);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int w = pair; w < total; w += npairs) {
+      const LinTile t = lw_tile(w, p);
+      // warp-uniform decision: tcgen05.ld below needs the whole warp
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase, abort, p.fault_site + 6))) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      const long long q = static_cast<long long>(t.q) * 256 + rank * 128 + quarter * 32 + lane;
+#pragma unroll 1
+      for (int c = set * 32; c < p.bn; c += 64) {
+        const int col = t.p * p.bn + c;
+        if (col >= p.P) break;  // warp-uniform
+        float a[32];
+        tmem_ld32(tbase + c, a);
+        if (q < p.Q) {
+          if (col + 32 <= p.P) {
+            lin_finish<OutT, 32>(p, q, col, a);
+          } else {
+            // P is a multiple of 8
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              if (col + i < p.P) lin_finish<OutT, 8>(p, q, col + i, a + i);
+          }
+        }
+        __syncwarp();
+      }
+      __syncwarp();
+      tc_fence_before();
+      if (lane == 0) mbar_arrive_cluster(acc_empty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+
+  __syncwarp();  // reconverge lanes that skipped the single-thread roles
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    ex_tmem_dealloc<2>(tmem_base);
+  }
+}
+
+// ------------------------------------------------------------------------------ skinny
+constexpr int LS_THREADS = 192;
+constexpr uint32_t LS_BUDGET = 108 * 1024;  // operand stages: two CTAs an SM
+constexpr int LS_MAX_SPLIT = 8;
+
+// BN rows of Q a tile.
+template <int BN>
+struct LsCfg {
+  static constexpr uint32_t kP = 128 * LIN_BK * 2;
+  // an MN-major Q takes whole boxes of 64 rows
+  static constexpr uint32_t kQ = (BN < 64 ? 64 : BN) * LIN_BK * 2;
+  static constexpr uint32_t kStage = kP + kQ;
+  static constexpr int kStages = LS_BUDGET / kStage > 8 ? 8 : static_cast<int>(LS_BUDGET / kStage);
+  static constexpr uint32_t kCols = BN < 32 ? 32 : BN;  // tensor memory columns
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + 256;
+  static_assert(kStages >= 2 && BN * 128 * 4 <= kStages * kStage, "the partial sums reuse the stages");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+template <typename OutT, int BN>
+__global__ void __launch_bounds__(LS_THREADS, 2)
+    linear_skinny_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
+  using C = LsCfg<BN>;
+  extern __shared__ uint8_t ls_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ls_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* done = empty + C::kStages;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int split = gridDim.x / p.p_tiles;  // CTAs of the cluster
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int p0 = static_cast<int>(blockIdx.x) / split * 128;
+  const long long q0 = static_cast<long long>(blockIdx.y) * BN;
+  const int kb0 = static_cast<int>(static_cast<long long>(p.nkb) * rank / split);
+  const int nkb = static_cast<int>(static_cast<long long>(p.nkb) * (rank + 1) / split) - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.p);
+    tma_prefetch_desc(&maps.q);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0u, issued_parity = 0u;
+      const uint32_t bytes = C::kP + (p.q_mn ? C::kQ : BN * 128u);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort, p.fault_site + 1)) break;
+        mbar_arrive_expect_tx(&full[stage], bytes);
+        const int kc = (kb0 + kb) * LIN_BK;
+        uint8_t* a_dst = smem + stage * C::kStage;
+        uint8_t* b_dst = a_dst + C::kP;
+        if (p.p_mn) {
+          tma_load_2d(a_dst, &maps.p, &full[stage], p0, kc);
+          tma_load_2d(a_dst + LIN_BOX_MN, &maps.p, &full[stage], p0 + 64, kc);
+        } else {
+          tma_load_2d(a_dst, &maps.p, &full[stage], kc, p0);
+        }
+        if (p.q_mn) {
+          for (uint32_t b = 0; b < C::kQ / LIN_BOX_MN; ++b)
+            tma_load_2d(b_dst + b * LIN_BOX_MN, &maps.q, &full[stage], static_cast<int>(q0) + b * 64, kc);
+        } else {
+          tma_load_2d(b_dst, &maps.q, &full[stage], kc, static_cast<int>(q0));
+        }
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // every load has landed before its memory is used again
+      volatile int never = 0;
+      for (int s = 0; s < C::kStages; ++s)
+        if ((issued >> s) & 1u) mbar_wait(&full[s], (issued_parity >> s) & 1u, &never, p.fault_site + 2);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = lin_idesc(128, BN, p.bf16 != 0, p.p_mn != 0, p.q_mn != 0);
+      const uint32_t a_step = p.p_mn ? 2048u : 32u, b_step = p.q_mn ? 2048u : 32u;
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait(&full[stage], phase, abort, p.fault_site + 3)) break;
+        tc_fence_after();
+        const uint32_t a_addr = smem_u32(smem + stage * C::kStage);
+        const uint32_t b_addr = a_addr + C::kP;
+        const uint64_t ad = p.p_mn ? sw128_mnmajor_desc(a_addr) : sw128_kmajor_desc(a_addr);
+        const uint64_t bd = p.q_mn ? sw128_mnmajor_desc(b_addr) : sw128_kmajor_desc(b_addr);
+#pragma unroll
+        for (int kk = 0; kk < LIN_BK / 16; ++kk)
+          tc_mma_bf16(tmem_base, ad + ((kk * a_step) >> 4), bd + ((kk * b_step) >> 4), idesc, (kb | kk) != 0 ? 1u : 0u);
+        tc_commit(&empty[stage]);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // also after a wait that gave up: what was issued completes
+      tc_commit(done);
+    }
+    __syncwarp();
+  }
+  // everyone waits for the last MMA (the producer's loads have landed by then:
+  // the MMAs read them, or its own wait saw them)
+  {
+    volatile int never = 0;
+    __syncwarp();
+    mbar_wait(done, 0u, &never, p.fault_site + 4);
+  }
+  __syncthreads();
+  tc_fence_after();
+  // partial sums to shared memory as [Q row][128], over the stages
+  float* part = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+    const int quarter = warp & 3;
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+    for (int c = 0; c < BN; c += 32) {
+      float a[32];
+      tmem_ld32(tbase + c, a);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c + i < BN) part[(c + i) * 128 + quarter * 32 + lane] = a[i];
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  // the cluster's CTAs share the outputs: four columns of a row each time,
+  // partial sums added in rank order
+  const uint32_t part_addr = smem_u32(part);
+  for (int i = rank * LS_THREADS + threadIdx.x; i < BN * 32; i += split * LS_THREADS) {
+    const int row = i >> 5, col = p0 + (i & 31) * 4;
+    if (q0 + row >= p.Q || col >= p.P) continue;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < split; ++s) {
+      const float4 v = ld_cluster_f4(map_to_rank(part_addr + static_cast<uint32_t>(i) * 16u, static_cast<uint32_t>(s)));
+      a[0] += v.x;
+      a[1] += v.y;
+      a[2] += v.z;
+      a[3] += v.w;
+    }
+    lin_finish<OutT, 4>(p, q0 + row, col, a);
+  }
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves while its partial sums are read
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kCols);
+  }
+}
+
+// ------------------------------------------------------------------------------ dp and dbias
+// dp = dy act'(pre), rounded to the operand type (skipped where dp is null), and
+// each block's column sums of the unrounded dp (skipped where part is null):
+// part[blockIdx.y][N].  Thread = 8 columns; a block walks over `rows` rows from
+// blockIdx.y * rows on.
+constexpr int LIN_DP_THREADS = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(LIN_DP_THREADS)
+    linear_dp_kernel(const T* __restrict__ dy, const T* __restrict__ pre, T* __restrict__ dp, float* __restrict__ part,
+                     long long M, int N, long long rows, int act) {
+  const int col = (blockIdx.x * LIN_DP_THREADS + threadIdx.x) * 8;
+  if (col >= N) return;
+  const long long r0 = blockIdx.y * rows, r1 = min(M, r0 + rows);
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+#pragma unroll 4
+  for (long long r = r0; r < r1; ++r) {
+    float d[8];
+    op_load<T, 8>(dy + r * N + col, d);
+    if (act != kActNone) {
+      float a[8];
+      op_load<T, 8>(pre + r * N + col, a);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] *= lin_act_grad(a[i], act);
+      if (dp != nullptr) op_store<T, 8>(dp + r * N + col, d);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += d[i];
+  }
+  if (part != nullptr) {
+    float* o = part + static_cast<long long>(blockIdx.y) * N + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = sum[i];
+  }
+}
+
+}  // namespace moe

@@ -218,25 +218,26 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_backward_kernel(const 
   }
 }
 
-// out[c] = sum over the parts, in order within each of 32 slices, then over the
-// slices: columns [0, H) are dgamma, [H, 2H) dbeta.
+// Sum of column c of part[parts][width], in order within each of 32 slices, then
+// over the slices: columns [0, H) go to a_out, the others to b_out (either may
+// be null).
 __global__ void __launch_bounds__(1024)
-    column_sum_kernel(const float* __restrict__ part, int parts, int H, float* __restrict__ dgamma,
-                      float* __restrict__ dbeta) {
+    column_sum_kernel(const float* __restrict__ part, int parts, int width, int H, float* __restrict__ a_out,
+                      float* __restrict__ b_out) {
   __shared__ float red[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float a = 0.f;
-  if (c < 2 * H)
-    for (int i = threadIdx.y; i < parts; i += 32) a += part[static_cast<long long>(i) * 2 * H + c];
+  if (c < width)
+    for (int i = threadIdx.y; i < parts; i += 32) a += part[static_cast<long long>(i) * width + c];
   red[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
   a = warp_sum(red[threadIdx.x][threadIdx.y]);
   const int col = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && col < 2 * H) {
+  if (threadIdx.x == 0 && col < width) {
     if (col < H) {
-      if (dgamma != nullptr) dgamma[col] = a;
-    } else if (dbeta != nullptr) {
-      dbeta[col - H] = a;
+      if (a_out != nullptr) a_out[col] = a;
+    } else if (b_out != nullptr) {
+      b_out[col - H] = a;
     }
   }
 }

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "clip.cuh"
+#include "linear.cuh"
 #include "norm.cuh"
 #include "route.cuh"
 #include "../../include/moe_ops.h"
@@ -159,6 +160,140 @@ void norm_bwd_dispatch(const NormBwdParams& p, int blocks, cudaStream_t s) {
     else if constexpr (VL == 1)
       norm_backward_kernel<T, VL, 16, false><<<blocks, threads(16), 0, s>>>(p);
   }
+}
+
+// ------------------------------------------------------------------------------ linear
+bool lin_ok(const moe_linear_desc* d) {
+  return d != nullptr && d->M >= 0 && d->M <= 0x7fffffffLL && d->N >= 1 && d->K >= 1 && d->act >= MOE_ACT_NONE &&
+         d->act <= MOE_ACT_GELU_TANH && op_type_ok(d->dtype) && (d->y_out == MOE_F32 || d->y_out == d->dtype);
+}
+moe_status lin_check(const moe_linear_desc* d) {
+  if (!lin_ok(d)) return MOE_ERR_INVALID_ARG;
+  return d->dtype == MOE_F32 || d->N % 8 != 0 || d->K % 8 != 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// One product out[Q, P] = f(sum over R): operand p is [P, R] (or, MN-major, lies
+// as [R, P]), operand q [Q, R] (or [R, Q]).
+struct LinProblem {
+  const void *p, *q;
+  bool p_mn, q_mn;
+  long long P, Q, R;
+};
+
+bool lin_map(CUtensorMap* m, const void* base, bool mn, long long rows, long long R, int box_rows) {
+  return mn ? make_map(m, base, R, rows, rows, LIN_BK) : make_map(m, base, rows, R, R, box_rows);
+}
+
+// Tile width of the wide kernel: the widest of those that give the shortest
+// last wave (a tile costs its width and about 32 columns' time besides).
+int lin_wide_bn(long long q_tiles, long long P, int pairs) {
+  int best = 256;
+  double cost = 0.0;
+  for (int bn = 256; bn >= 128; bn -= 32) {
+    const double c = static_cast<double>(cdiv(q_tiles * cdiv(P, bn), pairs)) * (bn + 32);
+    if (bn == 256 || c < cost) {
+      best = bn;
+      cost = c;
+    }
+  }
+  return best;
+}
+
+template <typename OutT>
+cudaError_t lin_launch_wide(const LinProblem& g, LinParams& p, cudaStream_t s) {
+  auto kern = linear_wide_kernel<OutT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(LW_SMEM));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(LW_THREADS);
+  cfg.dynamicSmemBytes = LW_SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static int pairs_cache[128] = {};
+  const int pairs = cluster_pairs(kern, cfg, pairs_cache);
+  const long long q_tiles = cdiv(g.Q, 256);
+  p.bn = lin_wide_bn(q_tiles, g.P, pairs);
+  p.q_tiles = static_cast<int>(q_tiles);
+  p.p_tiles = static_cast<int>(cdiv(g.P, p.bn));
+  LinMaps maps;
+  if (!lin_map(&maps.p, g.p, g.p_mn, g.P, g.R, p.bn / 2) || !lin_map(&maps.q, g.q, g.q_mn, g.Q, g.R, 128))
+    return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(pairs, q_tiles * p.p_tiles)));
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+template <typename OutT, int BN>
+cudaError_t lin_launch_skinny(const LinProblem& g, LinParams& p, cudaStream_t s) {
+  auto kern = linear_skinny_kernel<OutT, BN>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(LsCfg<BN>::kSmem));
+  if (e != cudaSuccess) return e;
+  p.bn = BN;
+  p.p_tiles = static_cast<int>(cdiv(g.P, 128));
+  p.q_tiles = static_cast<int>(cdiv(g.Q, BN));
+  // as many CTAs on the sum as two per SM allow, each with a few blocks of it
+  const long long tiles = static_cast<long long>(p.p_tiles) * p.q_tiles;
+  const int split = static_cast<int>(
+      std::max<long long>(1, std::min<long long>({LS_MAX_SPLIT, 2LL * num_sms() / tiles, p.nkb / 2})));
+  LinMaps maps;
+  if (!lin_map(&maps.p, g.p, g.p_mn, g.P, g.R, 128) || !lin_map(&maps.q, g.q, g.q_mn, g.Q, g.R, BN))
+    return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.p_tiles * split), static_cast<unsigned>(p.q_tiles));
+  cfg.blockDim = dim3(LS_THREADS);
+  cfg.dynamicSmemBytes = LsCfg<BN>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+template <typename OutT>
+moe_status lin_product(const LinProblem& g, LinParams p, cudaStream_t s) {
+  p.P = static_cast<int>(g.P);
+  p.Q = g.Q;
+  p.nkb = static_cast<int>(cdiv(g.R, LIN_BK));
+  p.p_mn = g.p_mn;
+  p.q_mn = g.q_mn;
+  const long long wide = cdiv(g.Q, 256) * cdiv(g.P, 256);
+  if (cdiv(g.Q, 256) * cdiv(g.P, 128) > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  cudaError_t e;
+  // few rows, or fewer than half the CTA pairs at work on 256 x 256 tiles
+  if (g.Q <= 128 || wide < num_sms() / 4) {
+    e = g.Q <= 16   ? lin_launch_skinny<OutT, 16>(g, p, s)
+        : g.Q <= 32 ? lin_launch_skinny<OutT, 32>(g, p, s)
+        : g.Q <= 64 ? lin_launch_skinny<OutT, 64>(g, p, s)
+                    : lin_launch_skinny<OutT, 128>(g, p, s);
+  } else {
+    e = lin_launch_wide<OutT>(g, p, s);
+  }
+  ++g_last_launches;
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status lin_product_of(int out_type, const LinProblem& g, const LinParams& p, cudaStream_t s) {
+  if (out_type == MOE_F32) return lin_product<float>(g, p, s);
+  return out_type == MOE_BF16 ? lin_product<__nv_bfloat16>(g, p, s) : lin_product<__half>(g, p, s);
+}
+
+// Blocks along the rows of the dp kernel: about eight a SM in all.
+long long lin_dp_parts(const moe_linear_desc& d) {
+  const long long across = cdiv(d.N, LIN_DP_THREADS * 8);
+  return std::max<long long>(1, std::min<long long>({d.M, cdiv(8LL * num_sms(), across), 65535}));
+}
+size_t lin_dp_bytes(const moe_linear_desc& d) {
+  return d.act == MOE_ACT_NONE ? 0 : round_up(static_cast<size_t>(d.M) * d.N * 2, kAlign);
 }
 
 // ------------------------------------------------------------------------------ clipping
@@ -340,10 +475,105 @@ moe_status moe_norm_backward(const moe_norm_desc* d, const void* dy, const void*
   }
   if (dgamma != nullptr || dbeta != nullptr) {
     column_sum_kernel<<<static_cast<unsigned>(cdiv(2LL * d->H, 32)), dim3(32, 32), 0, s>>>(
-        part, d->T > 0 ? blocks : 0, d->H, dgamma, dbeta);
+        part, d->T > 0 ? blocks : 0, 2 * d->H, d->H, dgamma, dbeta);
     ++g_last_launches;
   }
   return launched();
+}
+
+size_t moe_linear_workspace_size(const moe_linear_desc* d) {
+  (void)d;
+  return 0;  // split sums meet in the CTAs' shared memory
+}
+
+moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* weight, const float* bias,
+                      const void* residual, void* pre, void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  using namespace moe;
+  (void)ws;
+  (void)ws_bytes;
+  moe_status st = lin_check(d);
+  if (st != MOE_OK) return st;
+  g_last_launches = 0;
+  if (d->M == 0) return MOE_OK;
+  if (!ptr_ok(x) || !ptr_ok(weight) || !ptr_ok(y) || !aligned16(bias) || !aligned16(residual) || !aligned16(pre))
+    return MOE_ERR_INVALID_ARG;
+  LinParams p{};
+  p.bf16 = d->dtype == MOE_BF16;
+  p.bias = bias;
+  p.residual = residual;
+  p.pre = pre;
+  p.out = y;
+  p.act = d->act;
+  p.fault_site = 200;
+  const LinProblem g{weight, x, false, false, d->N, d->M, d->K};
+  return lin_product_of(d->y_out, g, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_linear_backward_workspace_size(const moe_linear_desc* d) {
+  using namespace moe;
+  if (lin_check(d) != MOE_OK) return 0;
+  return lin_dp_bytes(*d) + round_up(static_cast<size_t>(lin_dp_parts(*d)) * d->N * 4, kAlign);
+}
+
+moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, const void* pre, const void* x,
+                               const void* weight, void* dx, void* dweight, float* dbias, void* ws, size_t ws_bytes,
+                               moe_stream_t stream) {
+  using namespace moe;
+  moe_status st = lin_check(d);
+  if (st != MOE_OK) return st;
+  if (!aligned16(dx) || !aligned16(dweight) || !aligned16(dbias)) return MOE_ERR_INVALID_ARG;
+  const bool act = d->act != MOE_ACT_NONE;
+  if (d->M > 0 && (!ptr_ok(dy) || (act && !ptr_ok(pre)) || (dweight != nullptr && !ptr_ok(x)) ||
+                   (dx != nullptr && !ptr_ok(weight))))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws_fits(ws, ws_bytes, moe_linear_backward_workspace_size(d))) return MOE_ERR_INVALID_ARG;
+  g_last_launches = 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->M == 0) {
+    if (dweight != nullptr && cudaMemsetAsync(dweight, 0, static_cast<size_t>(d->N) * d->K * 2, s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    if (dbias != nullptr && cudaMemsetAsync(dbias, 0, static_cast<size_t>(d->N) * 4, s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  const void* dp = dy;
+  if (act || dbias != nullptr) {
+    void* to = act ? ws : nullptr;
+    float* part = dbias != nullptr ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + lin_dp_bytes(*d)) : nullptr;
+    const long long parts = lin_dp_parts(*d), rows = cdiv(d->M, parts);
+    const dim3 grid(static_cast<unsigned>(cdiv(d->N, LIN_DP_THREADS * 8)), static_cast<unsigned>(cdiv(d->M, rows)));
+    auto run = [&](auto v) {
+      using T = decltype(v);
+      linear_dp_kernel<T><<<grid, LIN_DP_THREADS, 0, s>>>(static_cast<const T*>(dy), static_cast<const T*>(pre),
+                                                          static_cast<T*>(to), part, d->M, d->N, rows, d->act);
+    };
+    if (d->dtype == MOE_BF16)
+      run(__nv_bfloat16());
+    else
+      run(__half());
+    ++g_last_launches;
+    if (dbias != nullptr) {
+      column_sum_kernel<<<static_cast<unsigned>(cdiv(d->N, 32)), dim3(32, 32), 0, s>>>(
+          part, static_cast<int>(grid.y), d->N, d->N, dbias, nullptr);
+      ++g_last_launches;
+    }
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if (act) dp = to;
+  }
+  LinParams p{};
+  p.bf16 = d->dtype == MOE_BF16;
+  p.act = kActNone;
+  if (dx != nullptr) {
+    p.out = dx;
+    p.fault_site = 210;
+    if ((st = lin_product_of(d->dtype, {weight, dp, true, false, d->K, d->M, d->N}, p, s)) != MOE_OK) return st;
+  }
+  if (dweight != nullptr) {
+    p.out = dweight;
+    p.fault_site = 220;
+    if ((st = lin_product_of(d->dtype, {x, dp, true, true, d->K, d->N, d->M}, p, s)) != MOE_OK) return st;
+  }
+  return MOE_OK;
 }
 
 size_t moe_clip_grads_workspace_size(const moe_grad_tensor* list, int32_t count) {

@@ -91,6 +91,36 @@ def test_norm_refuses():
     assert moe.moe_norm(moe.norm_desc(0, 64), None, None, None, None, None, None, 0) == moe.MOE_OK
 
 
+def test_linear_refuses():
+    ok = dict(M=4, N=64, K=64)
+    ptrs = [FAKE, FAKE, None, None, None, FAKE]
+    for kw, st in ((dict(M=-1), BAD), (dict(N=0), BAD), (dict(K=0), BAD), (dict(M=1 << 31), BAD), (dict(N=63), UNSUP),
+                   (dict(K=12), UNSUP), (dict(dtype="f32"), UNSUP), (dict(dtype="bf16", y_out="f16"), BAD)):
+        d = moe.linear_desc(**{**ok, **kw})
+        assert moe.moe_linear(d, *ptrs, None, None, 0) == st, kw
+        assert moe.moe_linear_backward_workspace_size(d) == 0, kw
+        assert moe.moe_linear_backward(d, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 30, 0) == st, kw
+    d = moe.linear_desc(**ok)
+    for act in (-1, 5):
+        d.act = act
+        assert moe.moe_linear(d, *ptrs, None, None, 0) == BAD
+    d = moe.linear_desc(**ok, act="silu")
+    for i, v in ((0, None), (1, None), (5, None), (0, FAKE + 8), (2, FAKE + 4), (3, FAKE + 2), (4, FAKE + 8)):
+        bad = list(ptrs)
+        bad[i] = v
+        assert moe.moe_linear(d, *bad, None, None, 0) == BAD, (i, v)
+    n = moe.moe_linear_backward_workspace_size(d)
+    good = [FAKE] * 7
+    for i in (0, 1, 2, 3):  # dy, pre, x, weight
+        bad = list(good)
+        bad[i] = None
+        assert moe.moe_linear_backward(d, *bad, FAKE, n, 0) == BAD, i
+    assert moe.moe_linear_backward(d, *good, FAKE, n - 1, 0) == BAD
+    assert moe.moe_linear_backward(d, *good, FAKE + 16, n, 0) == BAD
+    assert moe.moe_linear_backward(d, *good, None, n, 0) == BAD
+    assert moe.moe_linear(moe.linear_desc(0, 64, 64), None, None, None, None, None, None, None, None, 0) == moe.MOE_OK
+
+
 def test_clip_refuses():
     t = [torch.zeros(5), torch.zeros(3, dtype=torch.bfloat16)]
     lst = moe.tensor_list(t)
@@ -169,6 +199,19 @@ def test_oracle_norm_gradients(kind):
     if kind == "layer":
         ref = torch.nn.functional.layer_norm(x, (9,), gamma, beta, 1e-5)
         assert (y - ref).abs().max() < 1e-12
+
+
+@pytest.mark.parametrize("kind", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+def test_oracle_linear_gradients(kind):
+    g = torch.Generator().manual_seed(6)
+    x, w = torch.randn(4, 6, generator=g, dtype=F64), torch.randn(5, 6, generator=g, dtype=F64)
+    b, dy = torch.randn(5, generator=g, dtype=F64), torch.randn(4, 5, generator=g, dtype=F64)
+    pre, _ = oo.linear(x, w, b, None, kind)
+    _, dx, dw, db = oo.linear_backward(dy, pre, x, w, kind)
+    loss = lambda x, w, b: (oo.linear(x, w, b, None, kind)[1] * dy).sum()  # noqa: E731
+    assert (dx - _differences(lambda v: loss(v, w, b), x)).abs().max() < 1e-7
+    assert (dw - _differences(lambda v: loss(x, v, b), w)).abs().max() < 1e-7
+    assert (db - _differences(lambda v: loss(x, w, v), b)).abs().max() < 1e-7
 
 
 def test_oracle_clip():
