@@ -161,6 +161,13 @@ def _stream(stream):
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
 
+    if torch.cuda.is_initialized():
+        # the current stream's handle without building a Stream object: 0.3 of
+        # the 4.2 us that the two public calls below take
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            pass
     return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
 
 

@@ -60,37 +60,37 @@ RouteParams route_params(const moe_route_desc& d) {
   return p;
 }
 
-template <typename T, int VL, int CH>
-void route_launch(const RouteParams& p, cudaStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(cdiv(p.T, ROUTE_WARPS));
-  route_kernel<T, VL, CH><<<blocks, ROUTE_WARPS * 32, static_cast<size_t>(ROUTE_WARPS) * p.E * 8, s>>>(p);
-}
+// Calls f(CH, VL as constants) with the fewest loads per lane that hold a row of E
+// elements: 16-byte loads where the rows are made of whole ones, else one element
+// a load.
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
 
-// The fewest loads per lane that hold the row; 16-byte loads where the rows
-// are made of whole ones, else one element a load.
-template <typename T>
-void route_dispatch(const RouteParams& p, cudaStream_t s) {
+template <typename T, typename F>
+void route_dispatch(int E, F f) {
   constexpr int V = kVec<T>;
-  if (p.E % V == 0) {
-    switch (cdiv(p.E, 32 * V)) {
-      case 1: return route_launch<T, V, 1>(p, s);
-      case 2: return route_launch<T, V, 2>(p, s);
-      case 3: return route_launch<T, V, 3>(p, s);
-      case 4: return route_launch<T, V, 4>(p, s);
+  if (E % V == 0) {
+    switch (cdiv(E, 32 * V)) {
+      case 1: return f(Const<V>(), Const<1>());
+      case 2: return f(Const<V>(), Const<2>());
+      case 3: return f(Const<V>(), Const<3>());
+      case 4: return f(Const<V>(), Const<4>());
     }
     if constexpr (V == 4) {
-      switch (cdiv(p.E, 32 * V)) {
-        case 5: return route_launch<T, V, 5>(p, s);
-        case 6: return route_launch<T, V, 6>(p, s);
-        case 7: return route_launch<T, V, 7>(p, s);
-        default: return route_launch<T, V, 8>(p, s);
+      switch (cdiv(E, 32 * V)) {
+        case 5: return f(Const<V>(), Const<5>());
+        case 6: return f(Const<V>(), Const<6>());
+        case 7: return f(Const<V>(), Const<7>());
+        default: return f(Const<V>(), Const<8>());
       }
     }
   }
-  if (p.E <= 128) return route_launch<T, 1, 4>(p, s);
-  if (p.E <= 256) return route_launch<T, 1, 8>(p, s);
-  if (p.E <= 512) return route_launch<T, 1, 16>(p, s);
-  return route_launch<T, 1, 32>(p, s);
+  if (E <= 128) return f(Const<1>(), Const<4>());
+  if (E <= 256) return f(Const<1>(), Const<8>());
+  if (E <= 512) return f(Const<1>(), Const<16>());
+  return f(Const<1>(), Const<32>());
 }
 
 // ------------------------------------------------------------------------------ norms
@@ -389,7 +389,15 @@ moe_status moe_route(const moe_route_desc* d, const void* logits, const float* b
   p.bias = bias;
   p.idx = idx;
   p.w = w;
-  with_type(d->dtype, [&](auto v) { route_dispatch<decltype(v)>(p, reinterpret_cast<cudaStream_t>(stream)); });
+  const unsigned blocks = static_cast<unsigned>(cdiv(d->T, ROUTE_WARPS));
+  const size_t smem = static_cast<size_t>(ROUTE_WARPS) * route_warp_bytes(d->E, d->keep_groups < d->groups);
+  with_type(d->dtype, [&](auto v) {
+    using T = decltype(v);
+    route_dispatch<T>(d->E, [&](auto vl, auto ch) {
+      route_kernel<T, decltype(vl)::value, decltype(ch)::value>
+          <<<blocks, ROUTE_WARPS * 32, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    });
+  });
   g_last_launches = 1;
   return launched();
 }
@@ -407,10 +415,10 @@ moe_status moe_route_backward(const moe_route_desc* d, const void* logits, const
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   with_type(d->dtype, [&](auto v) {
     using T = decltype(v);
-    if (d->E % kVec<T> == 0)
-      route_backward_kernel<T, kVec<T>><<<blocks, ROUTE_WARPS * 32, 0, s>>>(p, idx, dw, static_cast<T*>(dlogits));
-    else
-      route_backward_kernel<T, 1><<<blocks, ROUTE_WARPS * 32, 0, s>>>(p, idx, dw, static_cast<T*>(dlogits));
+    route_dispatch<T>(d->E, [&](auto vl, auto ch) {
+      route_backward_kernel<T, decltype(vl)::value, decltype(ch)::value>
+          <<<blocks, ROUTE_WARPS * 32, 0, s>>>(p, idx, dw, static_cast<T*>(dlogits));
+    });
   });
   g_last_launches = 1;
   return launched();

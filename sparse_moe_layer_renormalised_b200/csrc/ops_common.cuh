@@ -116,10 +116,11 @@ __device__ __forceinline__ V warp_sum(V v) {
   return v;
 }
 
+// Largest value of the warp (no NaN), by the hardware's reduction.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 }  // namespace moe

@@ -6,14 +6,20 @@
 // the top-k does not run k arg-max rounds over all keys: the k-th largest of
 // the 32 lanes' own maxima (one 32-wide sort) is a lower bound of the k-th key,
 // and only the few keys at or above it (22 of 896 at k = 16, on average) are
-// compacted into shared memory and sorted, 32 at a time.
+// listed and sorted, 32 at a time.  For the same reason sigmoid + bias keys are
+// first formed with one hardware tanh each, to 2.6e-4, and exactly enough to be
+// sorted for the candidates alone.
 //
 // Exact order from fp32 arithmetic: the fp32 keys carry an error of at most
 // route_tol; where two neighbours in the sorted list (or the last chosen and
-// the first left out) are nearer than twice that, and are not equal in both
-// logit and bias, the warp selects again with fp64 keys (route_exact).  At
-// k = 16 of 896 with normal logits about one row in a thousand does so.
+// one left out) are nearer than twice that, and are not equal in both logit and
+// bias, the warp orders the candidates again by fp64 keys, and likewise the
+// groups where the last kept one is as near.  At k = 16 of 896 with normal logits and
+// sigmoid scores about one row in a thousand does so, with softmax scores several
+// in a hundred.
 #pragma once
+
+#include <cfloat>
 
 #include "ops_common.cuh"
 #include "routing.cuh"
@@ -47,10 +53,17 @@ __device__ __forceinline__ float f32_unorder(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
 }
 
-// Bound of the error of an fp32 key: the score's (fast exponential and
-// reciprocal; under 3e-7 of the largest score of the row, measured against
-// 64 bits, with a margin of three) and the rounding of score + bias.
-__device__ __forceinline__ float route_tol(float smax, float key) { return 1e-6f * smax + 1.5e-7f * fabsf(key); }
+// Bound of the error of an fp32 key, score (at most smax in the row) plus bias.
+// The score, in steps of 2^-23 of smax: sigmoid: s (1 - s) times the fast
+// exponential's 2 + 1.173 |l|, at most 0.63, half for 1 + e and 2 for the fast
+// division: 3.2, 3.8e-7.  Softmax: at most 2 for the exponential and the
+// difference l - m beside it (the largest of e^-d (2 + 1.67 d)); the sum's, which
+// scales all scores: the exponentials' weighted mean, 2 + 1.67 * ln 1024, and 14
+// roundings of 2^-24 in its tree; 1 for the reciprocal: 24, 2.9e-6.  The sum with
+// the bias rounds by 2^-24.
+__device__ __forceinline__ float route_tol(int softmax, float smax, float key) {
+  return (softmax ? 3e-6f : 4e-7f) * smax + 7e-8f * fabsf(key);
+}
 
 // e^(l - m) over the row's maximum m; the limit where m is infinite.
 __device__ __forceinline__ float route_exp(float l, float m) {
@@ -122,202 +135,252 @@ __device__ __forceinline__ unsigned long long route_merge(unsigned long long top
   return hi;
 }
 
-// Selection of one token in fp64, straight from the definition: lane j gets
-// the j-th expert.  Called by whole warps, for the few rows whose fp32 keys are
-// too near to be told apart.
+// Sum of e^(l - m) over the row in fp64 (limits as in route_exp), in all lanes.
 template <typename T>
-__device__ __noinline__ int route_exact(const RouteParams& p, const T* row, int lane) {
-  const int E = p.E;
-  double m = -INFINITY;
-  for (int e = lane; e < E; e += 32) m = fmax(m, static_cast<double>(route_logit(op_f32(row[e]))));
+__device__ __noinline__ double route_sum64(const T* row, int E, double m, int lane) {
+  double z[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int e0 = lane; e0 < E; e0 += 128) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-  double z = 0.0;
-  if (p.softmax) {
-    for (int e = lane; e < E; e += 32) {
-      const double l = route_logit(op_f32(row[e]));
-      z += isinf(m) ? (l == m && m > 0 ? 1.0 : 0.0) : exp(l - m);
-    }
-    z = warp_sum(z);
-  }
-  double key[32];   // keys of experts lane, lane + 32, ...
-  uint32_t live = 0u;
-  for (int i = 0; i < 32; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = -INFINITY;
-    if (e >= E) continue;
-    const double l = route_logit(op_f32(row[e]));
-    live |= 1u << i;
-    if (isinf(l) && l < 0) continue;
-    double s;
-    if (p.softmax)
-      s = (isinf(m) ? (l == m ? 1.0 : 0.0) : exp(l - m)) / z;
-    else
-      s = 1.0 / (1.0 + exp(-l));
-    // without a bias the logits themselves order the experts
-    const double kk = p.bias != nullptr ? s + static_cast<double>(p.bias[e]) : l;
-    key[i] = kk == kk ? kk : -INFINITY;
-  }
-  uint32_t kept = 0xffffffffu;
-  if (p.keep < p.groups) {
-    double mine = -INFINITY;  // lane g: score of group g
-    for (int g = 0; g < p.groups; ++g) {
-      double a = -INFINITY, b = -INFINITY;
-      for (int e = g * p.gsize + lane; e < (g + 1) * p.gsize; e += 32) {
-        const double l = route_logit(op_f32(row[e]));
-        if (isinf(l) && l < 0) continue;
-        double s;
-        if (p.softmax)
-          s = (isinf(m) ? (l == m ? 1.0 : 0.0) : exp(l - m)) / z;
-        else
-          s = 1.0 / (1.0 + exp(-l));
-        double v = s + (p.bias != nullptr ? static_cast<double>(p.bias[e]) : 0.0);
-        if (p.bias == nullptr && p.gtop == 1) v = l;
-        if (!(v == v)) continue;
-        if (v > a) {
-          b = a;
-          a = v;
-        } else if (v > b) {
-          b = v;
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const double oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
-        if (oa > a) {
-          b = fmax(a, ob);
-          a = oa;
-        } else {
-          b = fmax(b, oa);
-        }
-      }
-      const double score = p.gtop == 2 && !(isinf(b) && b < 0) ? a + b : a;
-      if (lane == g) mine = score;
-    }
-    int rank = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const double o = __shfl_sync(0xffffffffu, mine, g);
-      rank += (o > mine || (o == mine && g < lane)) ? 1 : 0;
-    }
-    kept = __ballot_sync(0xffffffffu, lane < p.groups && rank < p.keep);
-    for (int i = 0; i < 32; ++i) {
-      const unsigned e = lane + 32 * i;
-      if (((live >> i) & 1u) && !((kept >> ((e * p.gmagic) >> 20)) & 1u)) live &= ~(1u << i);
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + 32 * i;
+      const double l = e < E ? static_cast<double>(route_logit(op_f32(row[e]))) : -INFINITY;
+      z[i] += isinf(m) ? (l == m && m > 0 ? 1.0 : 0.0) : exp(l - m);
     }
   }
-  int mine = 0;
-  for (int j = 0; j < p.k; ++j) {
-    double bk = -INFINITY;
-    int be = 0x7fffffff;
-    for (int i = 0; i < 32; ++i) {
-      const int e = lane + 32 * i;
-      if (((live >> i) & 1u) && (key[i] > bk || (key[i] == bk && e < be))) {
-        bk = key[i];
-        be = e;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double ok = __shfl_xor_sync(0xffffffffu, bk, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (ok > bk || (ok == bk && oe < be)) {
-        bk = ok;
-        be = oe;
-      }
-    }
-    if ((be & 31) == lane) live &= ~(1u << (be >> 5));
-    if (lane == j) mine = be;
-  }
-  return mine;
+  return warp_sum((z[0] + z[1]) + (z[2] + z[3]));
 }
+
+// The key of an unmasked logit l in fp64; z is route_sum64's (softmax only).
+__device__ __noinline__ double route_key64(int softmax, float l, float b, double m, double z) {
+  const double x = l;
+  const double s = softmax ? (isinf(m) ? (x == m ? 1.0 : 0.0) : exp(x - m)) / z : 1.0 / (1.0 + exp(-x));
+  return s + static_cast<double>(b);
+}
+
+// An expert with its fp64 key; a larger key, then a lower expert, comes first.
+struct Ranked {
+  double v;
+  int e;
+};
+__device__ __forceinline__ bool before(const Ranked& a, const Ranked& b) {
+  return a.v > b.v || (a.v == b.v && a.e < b.e);
+}
+__device__ __forceinline__ Ranked shfl_xor(const Ranked& r, int j) {
+  return {__shfl_xor_sync(0xffffffffu, r.v, j), __shfl_xor_sync(0xffffffffu, r.e, j)};
+}
+__device__ __forceinline__ Ranked cmpx(const Ranked& r, int lane, int j, bool up) {
+  const Ranked o = shfl_xor(r, j);
+  return (((lane & j) == 0) == up) == before(r, o) ? r : o;
+}
+
+// The candidates in the order of their fp64 keys: lane j gets the j-th expert
+// (-1: none).  32 at a time are sorted and merged into the 32 best.
+template <typename T>
+__device__ __noinline__ int route_resolve(const RouteParams& p, const T* row, const uint16_t* cand, int cnt, double m,
+                                          double z, int lane) {
+  Ranked top{-INFINITY, 0x7fffffff - 31 + lane};
+  for (int at = 0; at < cnt; at += 32) {
+    Ranked r{-INFINITY, 0x7fffffff - 63 + lane};  // (never equal to another lane's)
+    if (at + lane < cnt) {
+      r.e = cand[at + lane];
+      const double v = route_key64(p.softmax, route_logit(op_f32(row[r.e])), p.bias[r.e], m, z);
+      if (v == v) r.v = v;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll 1
+      for (int j = k >> 1; j > 0; j >>= 1) r = cmpx(r, lane, j, (lane & k) == 0);
+    const Ranked o{__shfl_sync(0xffffffffu, r.v, 31 - lane), __shfl_sync(0xffffffffu, r.e, 31 - lane)};
+    if (before(o, top)) top = o;
+#pragma unroll 1
+    for (int j = 16; j > 0; j >>= 1) top = cmpx(top, lane, j, true);
+  }
+  return top.e < ROUTE_MAX_E ? top.e : -1;
+}
+
+// Bit mask of the kept groups.  score: lane g's group score.  Equal scores go to
+// the lower group.
+template <typename V>
+__device__ __forceinline__ uint32_t route_keep(V score, int groups, int keep, int lane) {
+  int rank = 0;
+  for (int o = 0; o < groups; ++o) {
+    const V so = __shfl_sync(0xffffffffu, score, o);
+    rank += (so > score || (so == score && o < lane)) ? 1 : 0;
+  }
+  return __ballot_sync(0xffffffffu, lane < groups && rank < keep);
+}
+
+// The kept groups from fp64 scores: only the values of a group that fp32 puts
+// within twice the error of the last one that counts are formed again.
+template <typename T>
+__device__ __noinline__ uint32_t route_keep64(const RouteParams& p, const T* row, const float* val, float smax, double m,
+                                              double z, int lane, int lpg) {
+  const int g = lane / lpg, sub = lane - g * lpg;
+  float a = -INFINITY, b = -INFINITY;
+  if (g < p.groups) {
+    for (int j = sub; j < p.gsize; j += lpg) {
+      const float v = val[g * p.gsize + j];
+      b = fmaxf(b, fminf(a, v));
+      a = fmaxf(a, v);
+    }
+  }
+  for (int o = lpg >> 1; o > 0; o >>= 1) {
+    const float oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+    b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+    a = fmaxf(a, oa);
+  }
+  float thr = p.gtop == 2 ? b : a;
+  thr = fmaxf(thr - 2.f * route_tol(p.softmax, smax, thr), -FLT_MAX);
+  double a64 = -INFINITY, b64 = -INFINITY;
+  if (g < p.groups) {
+    for (int j = sub; j < p.gsize; j += lpg) {
+      const int e = g * p.gsize + j;
+      if (!(val[e] >= thr)) continue;
+      const double v = route_key64(p.softmax, route_logit(op_f32(row[e])), p.bias != nullptr ? p.bias[e] : 0.f, m, z);
+      b64 = fmax(b64, fmin(a64, v));
+      a64 = fmax(a64, v);
+    }
+  }
+  __syncwarp();
+  for (int o = lpg >> 1; o > 0; o >>= 1) {
+    const double oa = __shfl_xor_sync(0xffffffffu, a64, o), ob = __shfl_xor_sync(0xffffffffu, b64, o);
+    b64 = fmax(fmax(b64, ob), fmin(a64, oa));
+    a64 = fmax(a64, oa);
+  }
+  double score = p.gtop == 2 && !(isinf(b64) && b64 < 0) ? a64 + b64 : a64;
+  score = __shfl_sync(0xffffffffu, score, (lane * lpg) & 31);
+  return route_keep(score, p.groups, p.keep, lane);
+}
+
+// Bytes of shared memory a warp uses: two lists of 32 sort keys and one of 32
+// (logit, bias), then the candidates' numbers or, before them, the keys that the
+// groups are ranked by.
+constexpr int ROUTE_LISTS = 768;
+__host__ __device__ constexpr int route_warp_bytes(int E, bool grouped) {
+  return ROUTE_LISTS + (E * (grouped ? 4 : 2) + 15) / 16 * 16;
+}
+
+// tanh by the hardware's approximation: relative error up to 2^-11.
+__device__ __forceinline__ float tanh_approx(float x) {
+  float y;
+  asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Bound of the error of 0.5 tanh_approx(l / 2) + bias, which orders the experts
+// as sigmoid(l) + bias does.
+__device__ __forceinline__ float route_coarse_tol(float key) { return 2.6e-4f + 1.5e-7f * fabsf(key); }
 
 // CH loads of VL elements per lane; expert of value (c, i): (c * 32 + lane) * VL + i.
 template <typename T, int VL, int CH>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(ROUTE_WARPS * 32, 8) route_kernel(const RouteParams p) {
   constexpr int NV = VL * CH;
-  extern __shared__ unsigned long long route_smem[];  // per warp: E candidates (the group scores before them)
+  extern __shared__ __align__(16) uint8_t route_smem[];
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const long long t = static_cast<long long>(blockIdx.x) * ROUTE_WARPS + warp;
   if (t >= p.T) return;
   const int E = p.E, k = p.k;
+  const bool biased = p.bias != nullptr;
+  const bool grouped = p.keep < p.groups;
   const T* row = static_cast<const T*>(p.logits) + t * E;
-  unsigned long long* cand = route_smem + static_cast<size_t>(warp) * E;
+  uint8_t* smem = route_smem + warp * route_warp_bytes(E, grouped);
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(smem);  // [64]
+  float2* list_lb = reinterpret_cast<float2*>(smem + 512);                 // [32]
+  uint16_t* cand = reinterpret_cast<uint16_t*>(smem + ROUTE_LISTS);
+  float* val = reinterpret_cast<float*>(smem + ROUTE_LISTS);
 
+  // logits; NaN as -inf, also where the row ends
   float key[NV];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int e0 = (c * 32 + lane) * VL;
     if (e0 < E) {
       op_load<T, VL>(row + e0, key + c * VL);
+#pragma unroll
+      for (int i = 0; i < VL; ++i) key[c * VL + i] = fmaxf(key[c * VL + i], -INFINITY);
     } else {
 #pragma unroll
       for (int i = 0; i < VL; ++i) key[c * VL + i] = -INFINITY;
     }
   }
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    key[i] = route_logit(key[i]);
-    m = fmaxf(m, key[i]);
-  }
-  const bool biased = p.bias != nullptr;
-  const bool grouped = p.keep < p.groups;
-  float inv_z = 1.f;
-  float smax = 1.f;
-  if (p.softmax) {
-    m = warp_max(m);
-    if (biased || !p.renorm || (grouped && p.gtop == 2)) {
-      float z = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) z += route_exp(key[i], m);
-      z = warp_sum(z);
-      inv_z = z > 0.f ? 1.0f / z : 0.f;
-      smax = inv_z;
-    }
-  }
-  // scores, then keys; a NaN key never wins over a number
+  float m = -INFINITY, inv_z = 1.f, smax = 1.f;
   const bool need_scores = biased || (grouped && p.gtop == 2);
-  float gval[NV];  // what the group scores add up (only read when grouped)
-  if (need_scores) {
+  if (p.softmax && (need_scores || !p.renorm)) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
+    m = warp_max(m);
+    float z4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z4[i & 3] += route_exp(key[i], m);
+    const float z = warp_sum((z4[0] + z4[1]) + (z4[2] + z4[3]));
+    inv_z = z > 0.f ? 1.0f / z : 0.f;
+    smax = inv_z;
+  }
+  // keys: the logits themselves without a bias; score + bias (-inf where masked,
+  // and a NaN never wins) to route_tol; or, for the plain case of sigmoid + bias,
+  // to route_coarse_tol, which is enough to find the candidates
+  const bool coarse = biased && !p.softmax && !grouped;
+  if (coarse) {
+    float least = INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) least = fminf(least, key[i]);
+    uint32_t gone = 0u;  // masked values of the lane
+    if (least == -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) gone |= key[i] == -INFINITY ? 1u << i : 0u;
+    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int e0 = (c * 32 + lane) * VL;
-      float b[VL];
+      if (e0 < E) {
+        float b[VL];
+        op_load_f32<VL>(p.bias + e0, b);
 #pragma unroll
-      for (int i = 0; i < VL; ++i) b[i] = 0.f;
-      if (biased && e0 < E) op_load_f32<VL>(p.bias + e0, b);
+        for (int i = 0; i < VL; ++i) key[c * VL + i] = fmaf(0.5f, tanh_approx(0.5f * key[c * VL + i]), b[i]);
+      }
+    }
+    if (gone != 0u) {
 #pragma unroll
-      for (int i = 0; i < VL; ++i) {
-        const float l = key[c * VL + i];
-        const float s = p.softmax ? route_exp(l, m) * inv_z : __fdividef(1.0f, 1.0f + __expf(-l));
-        float v = s + b[i];
-        if (l == -INFINITY || v != v) v = -INFINITY;
-        gval[c * VL + i] = v;
-        if (biased) key[c * VL + i] = v;
+      for (int i = 0; i < NV; ++i)
+        if ((gone >> i) & 1u) key[i] = -INFINITY;
+    }
+  } else if (need_scores) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int e0 = (c * 32 + lane) * VL;
+      if (e0 < E) {
+        float b[VL];
+#pragma unroll
+        for (int i = 0; i < VL; ++i) b[i] = 0.f;
+        if (biased) op_load_f32<VL>(p.bias + e0, b);
+#pragma unroll
+        for (int i = 0; i < VL; ++i) {
+          const float l = key[c * VL + i];
+          const float s = p.softmax ? route_exp(l, m) * inv_z : __fdividef(1.0f, 1.0f + __expf(-l));
+          float v = s + b[i];
+          if (l == -INFINITY || v != v) v = -INFINITY;
+          if (grouped) val[e0 + i] = v;
+          if (biased) key[c * VL + i] = v;
+        }
       }
     }
   } else if (grouped) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) gval[i] = key[i];
+    for (int c = 0; c < CH; ++c) {
+      const int e0 = (c * 32 + lane) * VL;
+#pragma unroll
+      for (int i = 0; i < VL; ++i)
+        if (e0 < E) val[e0 + i] = key[c * VL + i];
+    }
   }
 
-  bool near = false;
+  double z64 = 0.0;  // route_sum64's, once it is needed
   uint32_t kept = 0xffffffffu;
   if (grouped) {
-    float* val = reinterpret_cast<float*>(cand);
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int i = 0; i < VL; ++i) {
-        const int e = (c * 32 + lane) * VL + i;
-        if (e < E) val[e] = gval[c * VL + i];
-      }
     __syncwarp();
     // 32 / P lanes per group, P the power of two at or above the group count
-    int P = 1;
-    while (P < p.groups) P <<= 1;
-    const int lpg = 32 / P;
+    const int lpg = 32 >> (32 - __clz(p.groups - 1));
     const int g = lane / lpg, sub = lane - g * lpg;
     float a = -INFINITY, b = -INFINITY;
     if (g < p.groups) {
@@ -335,90 +398,151 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
     float score = p.gtop == 2 && b != -INFINITY ? a + b : a;
     score = __shfl_sync(0xffffffffu, score, (lane * lpg) & 31);
     if (lane >= p.groups) score = -INFINITY;
-    int rank = 0;
-    for (int o = 0; o < p.groups; ++o) {
-      const float so = __shfl_sync(0xffffffffu, score, o);
-      rank += (so > score || (so == score && o < lane)) ? 1 : 0;
-    }
-    const bool mine = lane < p.groups && rank < p.keep;
-    kept = __ballot_sync(0xffffffffu, mine);
+    kept = route_keep(score, p.groups, p.keep, lane);
     if (need_scores) {
+      const bool mine = (kept >> lane) & 1u;
       const float lo = -warp_max(mine ? -score : -INFINITY);
       const float hi = warp_max(mine || lane >= p.groups ? -INFINITY : score);
-      const float tol = p.gtop * (route_tol(smax, lo) + route_tol(smax, hi));
-      near = hi != -INFINITY && !(lo - hi > tol);
+      const float tol = p.gtop * (route_tol(p.softmax, smax, lo) + route_tol(p.softmax, smax, hi));
+      if (hi != -INFINITY && !(lo - hi > tol)) {
+        if (p.softmax) z64 = route_sum64(row, E, m, lane);
+        kept = route_keep64<T>(p, row, val, smax, m, z64, lane, lpg);
+      }
     }
+    const bool whole = VL == 1 || p.gsize % VL == 0;  // a load lies in one group
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+    for (int c = 0; c < CH; ++c) {
+      const unsigned e0 = (c * 32 + lane) * VL;  // (past E: -inf already, any group will do)
+      bool in = (kept >> (((e0 * p.gmagic) >> 20) & 31u)) & 1u;
 #pragma unroll
       for (int i = 0; i < VL; ++i) {
-        const unsigned e = (c * 32 + lane) * VL + i;
-        if (!((kept >> (((e * p.gmagic) >> 20) & 31u)) & 1u)) key[c * VL + i] = -INFINITY;  // (e >= E: -inf already)
+        if (!whole) in = (kept >> ((((e0 + i) * p.gmagic) >> 20) & 31u)) & 1u;
+        if (!in) key[c * VL + i] = -INFINITY;
       }
+    }
     __syncwarp();
   }
 
-  // lower bound of the k-th largest key
-  float lm = -INFINITY;
+  // lower bound of the k-th largest key: the k-th largest of the lanes' maxima,
+  // or, for k > 16, of two maxima a lane, over half its keys each (at k = 32 of
+  // 1000 that leaves 43 candidates instead of 110)
+  float lm = -INFINITY, lm2 = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) lm = fmaxf(lm, key[i]);
-  lm = warp_sort_desc(lm, lane);
-  float thr = __shfl_sync(0xffffffffu, lm, k - 1);
-  if (biased) thr -= 2.f * route_tol(smax, thr);
-  if (!(thr == thr)) thr = -INFINITY;
-  int cnt = 0;
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const float v = key[c * VL + i];
-      const bool in = v >= thr && v != -INFINITY;
-      const uint32_t mask = __ballot_sync(0xffffffffu, in);
-      if (in) cand[cnt + __popc(mask & ((1u << lane) - 1u))] = route_pack(v, (c * 32 + lane) * VL + i);
-      cnt += __popc(mask);
+  for (int i = 0; i < NV; i += 2) {
+    lm = fmaxf(lm, key[i]);
+    lm2 = fmaxf(lm2, key[i + 1]);
+  }
+  float thr = -INFINITY;
+  if (k <= 16) {
+    // largest value by largest value (equal ones go together, which only lowers
+    // the bound)
+    lm = fmaxf(lm, lm2);
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) {
+      thr = warp_max(lm);
+      if (lm == thr) lm = -INFINITY;
     }
+  } else {
+    lm = warp_sort_desc(lm, lane);
+    lm2 = __shfl_sync(0xffffffffu, warp_sort_desc(lm2, lane), 31 - lane);
+    lm = fmaxf(lm, lm2);
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) lm = cmpx(lm, lane, j, true);
+    thr = __shfl_sync(0xffffffffu, lm, k - 1);
+  }
+  if (biased) thr -= 2.f * (coarse ? route_coarse_tol(thr) : route_tol(p.softmax, smax, thr));
+  thr = fmaxf(thr, -FLT_MAX);  // never -inf (or inf - inf)
+  // the keys at or above it, by number
+  uint32_t hits = 0u;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) hits |= key[i] >= thr ? 1u << i : 0u;
+  int cnt = 0;
+  for (uint32_t has; (has = __ballot_sync(0xffffffffu, hits != 0u)) != 0u; cnt += __popc(has)) {
+    if (hits != 0u) {
+      const int i = __ffs(static_cast<int>(hits)) - 1;
+      hits &= hits - 1u;
+      cand[cnt + __popc(has & ((1u << lane) - 1u))] = static_cast<uint16_t>(((i / VL) * 32 + lane) * VL + i % VL);
+    }
+  }
   __syncwarp();
-  unsigned long long top = warp_sort_desc(lane < cnt ? cand[lane] : 0ull, lane);
-  unsigned long long drop = 0ull;
-  for (int at = 32; at < cnt; at += 32)
-    top = route_merge(top, warp_sort_desc(at + lane < cnt ? cand[at + lane] : 0ull, lane), lane, drop);
+  // their keys, sorted; lane j then holds the j-th (0: none) with its logit and bias
+  unsigned long long top = 0ull, drop = 0ull;
+  float l = -INFINITY, b = 0.f;
+  auto candidate = [&](int at) {
+    const int e = cand[at];
+    l = route_logit(op_f32(row[e]));
+    float v = l;
+    if (biased) {
+      b = p.bias[e];
+      v = (p.softmax ? route_exp(l, m) * inv_z : __fdividef(1.0f, 1.0f + __expf(-l))) + b;
+      if (v != v) v = -INFINITY;
+    }
+    return route_pack(v, e);
+  };
+  if (cnt <= 32) {
+    // the rank of each among them is its place
+    const unsigned long long mine = lane < cnt ? candidate(lane) : 0ull;
+    list[lane] = mine;
+    __syncwarp();
+    int rank = lane < cnt ? 0 : lane;
+    const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(list);
+#pragma unroll 4
+    for (int j = 0; 2 * j < cnt; ++j) {
+      const ulonglong2 o = l2[j];
+      // (an empty entry's rank stays: nothing is above its own place)
+      if (o.x > mine && mine != 0ull) ++rank;
+      if (o.y > mine && mine != 0ull) ++rank;
+    }
+    list[32 + rank] = mine;
+    list_lb[rank] = make_float2(l, b);
+    __syncwarp();
+    top = list[32 + lane];
+    const float2 lb = list_lb[lane];
+    l = lb.x;
+    b = lb.y;
+  } else {
+    for (int at = 0; at < cnt; at += 32) {
+      const unsigned long long mine = warp_sort_desc(at + lane < cnt ? candidate(at + lane) : 0ull, lane);
+      top = at == 0 ? mine : route_merge(top, mine, lane, drop);
+    }
+    l = top != 0ull ? route_logit(op_f32(row[route_expert(top)])) : -INFINITY;
+    b = biased && top != 0ull ? p.bias[route_expert(top)] : 0.f;
+  }
 
   int e = top != 0ull ? route_expert(top) : 0;
-  const int nsel = min(k, min(cnt, 32));  // chosen by key; the others by index
-  float l = top != 0ull ? route_logit(op_f32(row[e])) : -INFINITY;
+  const float kk = f32_unorder(static_cast<uint32_t>(top >> 32));
+  // chosen by key; the others by index.  (A candidate's key may be -inf: a NaN or
+  // -inf bias under a coarse threshold.)
+  const int nsel = min(k, __popc(__ballot_sync(0xffffffffu, top != 0ull && kk != -INFINITY)));
   if (biased) {
-    // neighbours that fp32 cannot order
-    const float kk = f32_unorder(static_cast<uint32_t>(top >> 32));
-    const float b = top != 0ull ? p.bias[e] : 0.f;
     const float k2 = __shfl_down_sync(0xffffffffu, kk, 1);
     const float l2 = __shfl_down_sync(0xffffffffu, l, 1);
     const float b2 = __shfl_down_sync(0xffffffffu, b, 1);
     // neighbours among the chosen: apart, or equal in logit and bias (then the
     // index has ordered them)
-    bool bad = lane + 1 < nsel && !(kk - k2 > 2.f * route_tol(smax, kk)) && !(l == l2 && b == b2);
-    if (nsel > 0) {
-      // the last chosen against all that were left out
-      const float kl = __shfl_sync(0xffffffffu, kk, nsel - 1);
-      const float ll = __shfl_sync(0xffffffffu, l, nsel - 1);
-      const float bl = __shfl_sync(0xffffffffu, b, nsel - 1);
-      const float tol = 2.f * route_tol(smax, kl);
-      bad |= lane >= nsel && top != 0ull && !(kl - kk > tol) && !(l == ll && b == bl);
-      bad |= drop != 0ull && !(kl - f32_unorder(static_cast<uint32_t>(drop >> 32)) > tol);
+    bool bad = lane + 1 < nsel && !(kk - k2 > 2.f * route_tol(p.softmax, smax, kk)) && !(l == l2 && b == b2);
+    // the last chosen against all that were left out
+    const int last = nsel > 0 ? nsel - 1 : 0;
+    const float kl = __shfl_sync(0xffffffffu, kk, last);
+    const float ll = __shfl_sync(0xffffffffu, l, last);
+    const float bl = __shfl_sync(0xffffffffu, b, last);
+    const float tol = 2.f * route_tol(p.softmax, smax, kl);
+    const bool beyond = nsel > 0 && drop != 0ull && !(kl - f32_unorder(static_cast<uint32_t>(drop >> 32)) > tol);
+    bad |= beyond || (nsel > 0 && lane >= nsel && top != 0ull && !(kl - kk > tol) && !(l == ll && b == bl));
+    if (__any_sync(0xffffffffu, bad)) {
+      if (p.softmax && z64 == 0.0) z64 = route_sum64(row, E, m, lane);
+      e = max(0, route_resolve<T>(p, row, cand, cnt, m, z64, lane));
+      l = lane < k ? route_logit(op_f32(row[e])) : -INFINITY;
     }
-    near = near || __any_sync(0xffffffffu, bad);
   }
-  if (near) {
-    e = route_exact<T>(p, row, lane);
-    l = lane < k ? route_logit(op_f32(row[e])) : -INFINITY;
-  } else if (nsel < k) {
+  if (nsel < k) {
     // masked experts of the kept groups fill up, in ascending order
     int have = nsel;
     for (int e0 = 0; e0 < E && have < k; e0 += 32) {
       const int x = e0 + lane;
       bool is = false;
-      float lx = -INFINITY;
       if (x < E && ((kept >> ((static_cast<unsigned>(x) * p.gmagic) >> 20)) & 1u)) {
-        lx = route_logit(op_f32(row[x]));
+        const float lx = route_logit(op_f32(row[x]));
         const float bx = biased ? p.bias[x] : 0.f;
         is = lx == -INFINITY || bx == -INFINITY || bx != bx;
       }
@@ -440,18 +564,28 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
 
 // Gradient of the weights.  One warp per token.  Sigmoid scores and renormalised
 // softmax scores reach the chosen logits only (the row is cleared and k values
-// are put in); plain softmax scores reach every logit, and the row is read.
-// Bound by the write of dlogits.
-template <typename T, int VL>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32)
+// are put in); plain softmax scores reach every logit, and the row is read once,
+// into registers.  Bound by the write of dlogits (and that read).
+template <typename T, int VL, int CH>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32, 8)
     route_backward_kernel(const RouteParams p, const int32_t* __restrict__ idx, const float* __restrict__ dw,
                           T* __restrict__ dl_out) {
+  constexpr int NV = VL * CH;
   const int lane = threadIdx.x & 31;
   const long long t = static_cast<long long>(blockIdx.x) * ROUTE_WARPS + (threadIdx.x >> 5);
   if (t >= p.T) return;
   const int E = p.E, k = p.k;
   const T* row = static_cast<const T*>(p.logits) + t * E;
   T* out = dl_out + t * E;
+  const bool dense = p.softmax && !p.renorm;
+  float v[NV];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int e0 = (c * 32 + lane) * VL;
+#pragma unroll
+    for (int i = 0; i < VL; ++i) v[c * VL + i] = dense ? -INFINITY : 0.f;
+    if (dense && e0 < E) op_load<T, VL>(row + e0, v + c * VL);
+  }
   int e = -1 - lane;  // distinct where there is none
   float d = 0.f, l = -INFINITY;
   if (lane < k) {
@@ -473,52 +607,42 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32)
     if (l != -INFINITY) d = dw[t * k + lane] * p.scale;
   }
   float dl = 0.f;
-  if (p.softmax && !p.renorm) {
-    // every lane's running maximum and sum, joined
+  if (dense) {
     float m = -INFINITY, z = 0.f;
-    for (int e0 = lane * VL; e0 < E; e0 += 32 * VL) {
-      float v[VL];
-      op_load<T, VL>(row + e0, v);
-      float mm = m;
 #pragma unroll
-      for (int i = 0; i < VL; ++i) {
-        v[i] = route_logit(v[i]);
-        mm = fmaxf(mm, v[i]);
-      }
-      z = m == mm ? z : z * route_exp(m, mm);
-      m = mm;
-#pragma unroll
-      for (int i = 0; i < VL; ++i) z += route_exp(v[i], m);
+    for (int i = 0; i < NV; ++i) {
+      v[i] = fmaxf(v[i], -INFINITY);  // NaN as masked
+      m = fmaxf(m, v[i]);
     }
-    const float mm = warp_max(m);
-    z = warp_sum(m == mm ? z : z * route_exp(m, mm));
-    m = mm;
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = route_exp(v[i], m);
+      z += v[i];
+    }
+    z = warp_sum(z);
     const float inv_z = z > 0.f ? 1.0f / z : 0.f;
     const float s = e >= 0 ? route_score(l, 1, m, inv_z) : 0.f;
     const float dot = warp_sum(s * d);
     dl = s * (d - dot);
     const float f = -dot * inv_z;
-    for (int e0 = lane * VL; e0 < E; e0 += 32 * VL) {
-      float v[VL];
-      op_load<T, VL>(row + e0, v);
 #pragma unroll
-      for (int i = 0; i < VL; ++i) v[i] = f * route_exp(route_logit(v[i]), m);
-      op_store<T, VL>(out + e0, v);
-    }
+    for (int i = 0; i < NV; ++i) v[i] *= f;
   } else {
     float pj;
     if (p.renorm) {
       pj = route_share(l, p.softmax);
       d -= warp_sum(pj * d);
     } else {
-      pj = route_score(l, 0, 0.f, 1.f);  // (sigmoid: softmax without renorm is above)
+      pj = route_score(l, 0, 0.f, 1.f);  // (sigmoid: softmax without renorm is dense)
     }
     // 1 - sigmoid(l) without cancellation
     dl = pj * d * (p.softmax ? 1.f : 1.0f / (1.0f + expf(l)));
-    float zero[VL];
+  }
 #pragma unroll
-    for (int i = 0; i < VL; ++i) zero[i] = 0.f;
-    for (int e0 = lane * VL; e0 < E; e0 += 32 * VL) op_store<T, VL>(out + e0, zero);
+  for (int c = 0; c < CH; ++c) {
+    const int e0 = (c * 32 + lane) * VL;
+    if (e0 < E) op_store<T, VL>(out + e0, v + c * VL);
   }
   __syncwarp();  // the row's stores come before the chosen experts'
   if (e >= 0) out[e] = op_from<T>(dl);

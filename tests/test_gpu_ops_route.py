@@ -151,6 +151,43 @@ def test_ties_go_to_the_lower_index(E, k):
             _check(few, bias, k, "f32", score=score, groups=8, keep_groups=5, group_top=2)
 
 
+def _many_reference(l, b, k, groups, keep, group_top, score):
+    """idx of many rows on the GPU in fp64 by stable sorts (finite logits)."""
+    l = l.double()
+    s = torch.sigmoid(l) if score == "sigmoid" else torch.softmax(l, 1)
+    key = l if b is None else s + b.double()
+    if groups > 1:
+        T, E = l.shape
+        val = s if b is None else key
+        best = val.view(T, groups, -1).sort(dim=2, descending=True).values[:, :, :group_top].sum(2)
+        kept = best.sort(dim=1, descending=True, stable=True).indices[:, :keep]
+        out = torch.ones(T, groups, dtype=torch.bool, device=l.device).scatter_(1, kept, False)
+        key = key.masked_fill(out.repeat_interleave(E // groups, 1), -INF)
+    return key.sort(dim=1, descending=True, stable=True).indices[:, :k]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,groups,keep,group_top", [(896, 16, 1, 1, 1), (896, 32, 1, 1, 1), (1000, 32, 1, 1, 1),
+                                                       (128, 8, 1, 1, 1), (256, 8, 8, 4, 2), (512, 24, 16, 7, 2)])
+def test_many_rows(score, E, k, groups, keep, group_top):
+    """Enough rows that every path of the selection is taken, the rare near ties among them."""
+    T = 16384
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        std = (1.5, 0.01, 6.0, 1.5)[seed]  # usual, nearly equal, saturated, and half-precision logits
+        l = torch.randn(T, E, generator=g, device="cuda") * std
+        dtype = "bf16" if seed == 3 else "f32"
+        l = l.to(DT[dtype])
+        b = torch.randn(E, generator=g, device="cuda") * 0.05
+        for bias in (b, None):
+            idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+            d = moe.route_desc(T, E, k, groups=groups, keep_groups=keep, group_top=group_top, score=score, dtype=dtype)
+            assert moe.moe_route(d, l, bias, idx, w) == moe.MOE_OK
+            assert moe.moe_device_error() == (moe.MOE_OK, 0)
+            want = _many_reference(l, bias, k, groups, keep, group_top, score)
+            assert int((idx.long() != want).any(1).sum()) == 0, (seed, bias is None)
+
+
 def test_deterministic_and_rows_independent():
     l = _logits(300, 896, 1)
     b = _bias(896, 2)
