@@ -1,13 +1,26 @@
 // Layer norm and RMS norm of rows, and their gradients.
 //
-// Forward: a row stays in registers between its one read and its one write, so
-// the variance is that of the centred values (no sum of squares minus square of
-// sums).  Rows of at most 128 16-byte vectors take a warp each, longer ones a
-// block.  Bound by the read and the write.
+// Both kernels run one block per SM.  Its threads form groups (a warp for short
+// rows, up to all of them for long ones) that each walk over rows of their own;
+// the rows come through a ring of shared-memory stages that bulk copies fill
+// several rows ahead, so that loads stay in flight while a row's sums are formed
+// and its barriers waited for.  (A block per row with the row in registers leaves
+// the memory idle there: 16384 x 7168 bf16 took 115 us forward against 71 for its
+// bytes.)  A thread has the same columns in all of its rows.
 //
-// Backward: a block keeps its columns of dgamma and dbeta in registers while it
-// walks over rows, writes them to the workspace once, and a second kernel adds
-// up the blocks' parts in a fixed order; x and dy are read once.
+// Rows are read and written in 16-byte windows of the memory they lie in: where
+// the row length is no multiple of a window, row t starts `a` elements into one,
+// a = t H mod VL (VL elements a window), and window v holds the columns
+// v VL - a ... + VL - 1.  The rows of a group all have the same `a`.  The first and
+// the last window of such a row hold columns of its neighbours too, which are
+// masked on reading and left alone on writing.
+//
+// Forward: the variance is that of the centred values (no sum of squares minus
+// square of sums).  Backward: x and dy are read once; the sums of dgamma and dbeta
+// stay in registers, the blocks' sums go to the workspace and a second kernel adds
+// them up in a fixed order.  Both are bound by memory, closely followed by their
+// arithmetic: hence the packed fp32 instructions, and four windows a thread, which
+// share the cost of a row's sums and barriers.
 #pragma once
 
 #include "ops_common.cuh"
@@ -16,228 +29,482 @@ namespace moe {
 
 struct NormParams {
   const void* x;
+  const void* dy;      // backward
   const float* gamma;  // may be null
-  const float* beta;   // may be null
-  void* y;
-  float* mean;  // may be null
-  float* rstd;  // may be null
+  const float* beta;   // may be null (forward)
+  void* out;           // y or dx
+  float* mean;         // forward: may be null; backward: null for RMS norm
+  float* rstd;         // forward: may be null
+  float* part;         // backward: [gridDim.x][2][H], the blocks' dgamma and dbeta
   long long T;
   int H;
   float eps, inv_h;
   int rms;
+  int tpg;         // threads of a group, whole warps
+  int groups;      // groups of a block
+  int walkers;     // groups of the grid that take rows: group i takes i, i + walkers, ...
+  int stages;      // of a group's ring
+  int row_bytes;   // of a row's windows in a stage
+  int par_floats;  // of gamma (and as many of beta) in shared memory; 0: read where they lie
 };
 
-constexpr int NORM_WARP_ROWS = 4;  // rows (warps) per block where a warp takes a row
+constexpr int kFaultNormWait = 16;
+constexpr int NORM_MAX_RING = 8;
+// Threads of a block, at most: 88 registers each forward, 128 backward.  (With 896
+// threads in two groups the backward pass of rows of 7168 had too few registers.)
+constexpr int NORM_FWD_THREADS = 704;
+constexpr int NORM_BWD_THREADS = 512;
 
-// Sum over the threads of a row (a warp or the block), the same bits in all of them.
-template <bool WARP>
-__device__ __forceinline__ float norm_row_sum(float v, float* red) {
-  v = warp_sum(v);
-  if constexpr (!WARP) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    v = warp_sum(lane < nw ? red[lane] : 0.f);
-  }
-  return v;
+// Bulk copy of `bytes` (a multiple of 16, both ends 16-byte aligned) into shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
-// NV loads of VL elements per thread of the row.
-template <typename T, int VL, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * NORM_WARP_ROWS : 1024) norm_kernel(const NormParams p) {
-  __shared__ float red[2][32];
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int tpr = WARP ? 32 : blockDim.x;
-  const long long t = WARP ? static_cast<long long>(blockIdx.x) * NORM_WARP_ROWS + (threadIdx.x >> 5) : blockIdx.x;
-  if (t >= p.T) return;  // whole warps (WARP) only
-  const T* x = static_cast<const T*>(p.x) + t * p.H;
-  T* y = static_cast<T*>(p.y) + t * p.H;
-  const int nvec = p.H / VL;
-  float v[NV][VL];
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = tid + i * tpr;
-    if (c < nvec) {
-      op_load<T, VL>(x + static_cast<long long>(c) * VL, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VL; ++j) v[i][j] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < VL; ++j) sum += v[i][j];
-  }
-  float mean = 0.f;
-  if (!p.rms) mean = norm_row_sum<WARP>(sum, red[0]) * p.inv_h;
-  float sq = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = tid + i * tpr < nvec;
-#pragma unroll
-    for (int j = 0; j < VL; ++j) {
-      v[i][j] -= mean;
-      if (in) sq = fmaf(v[i][j], v[i][j], sq);
-    }
-  }
-  const float rstd = 1.0f / sqrtf(norm_row_sum<WARP>(sq, red[1]) * p.inv_h + p.eps);
-  if (tid == 0) {
-    if (p.mean != nullptr) p.mean[t] = mean;
-    if (p.rstd != nullptr) p.rstd[t] = rstd;
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = tid + i * tpr;
-    if (c >= nvec) continue;
-    float g[VL], b[VL];
-#pragma unroll
-    for (int j = 0; j < VL; ++j) g[j] = 1.f, b[j] = 0.f;
-    if (p.gamma != nullptr) op_load_f32<VL>(p.gamma + c * VL, g);
-    if (p.beta != nullptr) op_load_f32<VL>(p.beta + c * VL, b);
-#pragma unroll
-    for (int j = 0; j < VL; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[j], b[j]);
-    op_store<T, VL>(y + static_cast<long long>(c) * VL, v[i]);
-  }
+// 16 bytes of shared memory.  (Through 32-bit addresses: with pointers the compiler
+// spent as many instructions on addresses as on the arithmetic.)
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 q;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(addr) : "memory");
+  return q;
 }
 
-// ------------------------------------------------------------------------------ backward
-struct NormBwdParams {
-  const void* dy;
-  const void* x;
-  const float* gamma;  // may be null
-  const float* mean;   // null for RMS norm
-  const float* rstd;
-  void* dx;
-  float* part;  // [gridDim.x][2][H]: the blocks' dgamma and dbeta
-  long long T;
-  int H;
-  float inv_h;
-};
+// Shared memory: [groups][ring] mbarriers, [groups][2][32] float2 for the row
+// sums, gamma and beta, then [groups][stages][operands] rows; the blocks' column
+// sums reuse the rows.
+__host__ __device__ constexpr size_t norm_head(int groups) {
+  return static_cast<size_t>(groups) * (NORM_MAX_RING * 8 + 2 * 32 * 8);
+}
+// gamma and beta lie in shared memory with this much before and behind them, so
+// that the first and last windows need no bounds; where a window has two quads of
+// them, the even quads lie before the odd ones, so that a warp reads neighbours
+// (in their own order each read is a two-way bank conflict).
+constexpr int NORM_PAD = 8;
 
-// Rows are taken by groups of tpr threads (a warp, or the whole block), block b
-// taking rows b * groups + group + i * gridDim.x * groups.
-template <typename T, int VL, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_backward_kernel(const NormBwdParams p) {
-  __shared__ float2 red[2][32];
-  extern __shared__ float norm_acc[];  // WARP: [2][H]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int groups = WARP ? blockDim.x >> 5 : 1;
-  const int tid = WARP ? lane : threadIdx.x;
-  const int tpr = WARP ? 32 : blockDim.x;
-  const int nvec = p.H / VL;
-  const bool rms = p.mean == nullptr;
-  float dg[NV][VL], db[NV][VL], gm[NV][VL];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = tid + i * tpr;
-#pragma unroll
-    for (int j = 0; j < VL; ++j) dg[i][j] = 0.f, db[i][j] = 0.f, gm[i][j] = 1.f;
-    if (p.gamma != nullptr && c < nvec) op_load_f32<VL>(p.gamma + c * VL, gm[i]);
-  }
-  int buf = 0;
-  for (long long t = static_cast<long long>(blockIdx.x) * groups + (WARP ? warp : 0); t < p.T;
-       t += static_cast<long long>(gridDim.x) * groups) {
-    const T* x = static_cast<const T*>(p.x) + t * p.H;
-    const T* dy = static_cast<const T*>(p.dy) + t * p.H;
-    T* dx = static_cast<T*>(p.dx) + t * p.H;
-    const float mean = rms ? 0.f : p.mean[t], rstd = p.rstd[t];
-    float xh[NV][VL], g[NV][VL];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = tid + i * tpr;
-      if (c < nvec) {
-        op_load<T, VL>(x + static_cast<long long>(c) * VL, xh[i]);
-        op_load<T, VL>(dy + static_cast<long long>(c) * VL, g[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VL; ++j) xh[i][j] = mean, g[i][j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < VL; ++j) {
-        xh[i][j] = (xh[i][j] - mean) * rstd;
-        dg[i][j] = fmaf(g[i][j], xh[i][j], dg[i][j]);
-        db[i][j] += g[i][j];
-        g[i][j] *= gm[i][j];
-        s1 += g[i][j];
-        s2 = fmaf(g[i][j], xh[i][j], s2);
-      }
+// A group's place and its ring of OPS operands (x, or x and dy).
+template <typename T, int OPS, int NW, bool ALIGNED, bool PAR>
+struct NormRing {
+  static constexpr int VL = kVec<T>;
+  static_assert(ALIGNED || PAR, "unaligned parameters are read from shared memory");
+  const NormParams& p;
+  int g, tid, lane, warp, a;
+  int v0;    // the thread's first window; the others follow 32 apart
+  int col0;  // its first column
+  uint64_t* bars;
+  float2* red;
+  uint8_t* ring;
+  uint32_t mine;       // shared address of the thread's first window of stage 0, operand 0
+  uint32_t par[2];     // and of gamma's two first quads for it
+  uint32_t stage_b, op_b;  // bytes of a stage, of an operand in it
+  long long first;
+
+  __device__ __forceinline__ NormRing(const NormParams& q, uint8_t* smem) : p(q) {
+    g = threadIdx.x / p.tpg;
+    tid = threadIdx.x - g * p.tpg;
+    lane = threadIdx.x & 31;
+    warp = tid >> 5;
+    bars = reinterpret_cast<uint64_t*>(smem) + g * NORM_MAX_RING;
+    red = reinterpret_cast<float2*>(smem + p.groups * NORM_MAX_RING * 8) + g * 64;
+    float* const par0 = reinterpret_cast<float*>(smem + norm_head(p.groups));
+    op_b = p.row_bytes;
+    stage_b = OPS * op_b;
+    ring = reinterpret_cast<uint8_t*>(par0 + (OPS == 1 ? 2 : 1) * p.par_floats) + static_cast<size_t>(g) * p.stages * stage_b;
+    const int gid = blockIdx.x * p.groups + g;
+    first = gid < p.walkers ? gid : p.T;
+    a = ALIGNED || first >= p.T ? 0 : static_cast<int>(first * p.H % VL);
+    v0 = warp * 32 * NW + lane;
+    col0 = v0 * VL - a;
+    mine = smem_u32(ring) + v0 * 16;
+    const int q0 = (NORM_PAD + col0) >> 2;  // the quad that the first column is in
+    par[0] = smem_u32(par0 + quad(q0));
+    par[1] = smem_u32(par0 + quad(q0 + 1));
+    if (tid == 0) {
+      for (int i = 0; i < p.stages; ++i) mbar_init(&bars[i], 1);
+      fence_mbar_init();
+      long long t = first;
+      for (int i = 0; i < p.stages && t < p.T; ++i, t += p.walkers) issue(t, i);
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if constexpr (!WARP) {
-      // two buffers: one barrier per row
-      if (lane == 0) red[buf][warp] = make_float2(s1, s2);
-      __syncthreads();
-      const float2 r = lane < (tpr >> 5) ? red[buf][lane] : make_float2(0.f, 0.f);
-      s1 = warp_sum(r.x);
-      s2 = warp_sum(r.y);
-      buf ^= 1;
-    }
-    s1 = rms ? 0.f : s1 * p.inv_h;
-    s2 *= p.inv_h;
+    if constexpr (PAR) {
+      const float* from[2] = {p.gamma, p.beta};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = tid + i * tpr;
-      if (c >= nvec) continue;
-#pragma unroll
-      for (int j = 0; j < VL; ++j) g[i][j] = rstd * (g[i][j] - s1 - xh[i][j] * s2);
-      op_store<T, VL>(dx + static_cast<long long>(c) * VL, g[i]);
-    }
-  }
-  float* part = p.part + static_cast<long long>(blockIdx.x) * 2 * p.H;
-  if constexpr (WARP) {
-    // the warps' sums in warp order
-    for (int w = 0; w < groups; ++w) {
-      if (warp == w) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = tid + i * tpr;
-          if (c >= nvec) continue;
-#pragma unroll
-          for (int j = 0; j < VL; ++j) {
-            float* a = norm_acc + c * VL + j;
-            a[0] = w == 0 ? dg[i][j] : a[0] + dg[i][j];
-            a[p.H] = w == 0 ? db[i][j] : a[p.H] + db[i][j];
+      for (int k = 0; k < (OPS == 1 ? 2 : 1); ++k) {
+        const float none = k == 0 ? 1.f : 0.f;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < p.par_floats / 4; i += blockDim.x) {
+          const int j = 4 * i - NORM_PAD;
+          float4 v = make_float4(none, none, none, none);
+          if (from[k] != nullptr) {
+            if (j >= 0 && j + 4 <= p.H) {
+              v = *reinterpret_cast<const float4*>(from[k] + j);
+            } else {
+              if (inside(j)) v.x = from[k][j];
+              if (inside(j + 1)) v.y = from[k][j + 1];
+              if (inside(j + 2)) v.z = from[k][j + 2];
+              if (inside(j + 3)) v.w = from[k][j + 3];
+            }
           }
+          *reinterpret_cast<float4*>(par0 + k * p.par_floats + quad(i)) = v;
         }
       }
-      __syncthreads();
     }
-    for (int c = threadIdx.x; c < 2 * p.H; c += blockDim.x) part[c] = norm_acc[c];
-  } else {
+  }
+  // Place of quad i of a parameter, in floats.
+  __device__ __forceinline__ int quad(int i) const {
+    return VL == 4 ? 4 * i : (i & 1) * (p.par_floats / 2) + (i >> 1) * 4;
+  }
+  // A last window that ends behind the tensor (the last row's; of very short rows
+  // also some before it) is not copied.
+  __device__ __forceinline__ bool cut(long long t) const {
+    return !ALIGNED && t * p.H - a + (a + p.H + VL - 1) / VL * VL > p.T * p.H;
+  }
+  // Copies of row t into a stage, by one thread of the group.
+  __device__ __forceinline__ void issue(long long t, int stage) {
+    const uint32_t windows = static_cast<uint32_t>(cut(t) ? (a + p.H) / VL : (a + p.H + VL - 1) / VL);
+    mbar_arrive_expect_tx(&bars[stage], OPS * windows * 16u);
+    if (windows != 0u) {
+      const long long at = t * p.H - a;
+      uint8_t* dst = ring + static_cast<size_t>(stage) * OPS * p.row_bytes;
+      bulk_load(dst, static_cast<const T*>(p.x) + at, windows * 16u, &bars[stage]);
+      if constexpr (OPS == 2) bulk_load(dst + p.row_bytes, static_cast<const T*>(p.dy) + at, windows * 16u, &bars[stage]);
+    }
+  }
+  __device__ __forceinline__ void bar() {
+    __syncwarp();
+    if (p.tpg > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(p.tpg) : "memory");
+  }
+  // Sum over the group, the same bits in all threads; buf: 0 and 1 in turn.
+  __device__ __forceinline__ float sum(float v, int buf) {
+    v = warp_sum(v);
+    if (p.tpg > 32) {
+      float* r = reinterpret_cast<float*>(red + buf * 32);
+      if (lane == 0) r[warp] = v;
+      bar();
+      v = warp_sum(lane < (p.tpg >> 5) ? r[lane] : 0.f);
+    }
+    return v;
+  }
+  // Two sums over a group of at most 16 warps, in two steps with a bar() between
+  // them: half the warp carries one each.
+  __device__ __forceinline__ float sum2_put(float u, float v, int buf) {
+    const bool low = lane < 16;
+    float keep = low ? u : v;
+    keep += __shfl_xor_sync(0xffffffffu, low ? v : u, 16);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = tid + i * tpr;
-      if (c >= nvec) continue;
+    for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+    if (p.tpg > 32 && (lane & 15) == 0) reinterpret_cast<float*>(red + buf * 32)[(lane & 16) + warp] = keep;
+    return keep;
+  }
+  __device__ __forceinline__ float2 sum2_get(float keep, int buf) {
+    if (p.tpg > 32) {
+      keep = (lane & 15) < (p.tpg >> 5) ? reinterpret_cast<const float*>(red + buf * 32)[lane] : 0.f;
 #pragma unroll
-      for (int j = 0; j < VL; ++j) {
-        part[c * VL + j] = dg[i][j];
-        part[p.H + c * VL + j] = db[i][j];
+      for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+    }
+    return make_float2(__shfl_sync(0xffffffffu, keep, 0), __shfl_sync(0xffffffffu, keep, 16));
+  }
+  __device__ __forceinline__ int col(int w) const { return col0 + w * 32 * VL; }  // of the thread's window w
+  __device__ __forceinline__ bool whole(int j0) const { return ALIGNED || (j0 >= 0 && j0 + VL <= p.H); }
+  __device__ __forceinline__ bool inside(int j) const { return j >= 0 && j < p.H; }
+  // window w of an operand of row t, at its shared address; columns outside the row as `none`
+  __device__ __forceinline__ void load(uint32_t addr, const void* base, long long t, int w, float none, F2* f) const {
+    op_unpack16<T>(ld_shared16(addr + w * 512), f);
+    const int j0 = col(w);
+    if (!whole(j0)) {
+      const T* row = static_cast<const T*>(base) + t * p.H;
+      const bool fetch = cut(t) && j0 + VL > p.H;
+#pragma unroll
+      for (int i = 0; i < VL; i += 2) {
+        float2 v = f2_get(f[i / 2]);
+        if (fetch) {
+          v.x = inside(j0 + i) ? op_f32(row[j0 + i]) : none;
+          v.y = inside(j0 + i + 1) ? op_f32(row[j0 + i + 1]) : none;
+        } else {
+          v.x = inside(j0 + i) ? v.x : none;
+          v.y = inside(j0 + i + 1) ? v.y : none;
+        }
+        f[i / 2] = f2(v.x, v.y);
       }
+    }
+  }
+  // `out`: the thread's first column in the row
+  __device__ __forceinline__ void store(T* out, int w, const F2* f) const {
+    const int j0 = col(w);
+    T* row = out - col0;
+    if (whole(j0)) {
+      *reinterpret_cast<uint4*>(out + w * 32 * VL) = op_pack16<T>(f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VL; i += 2) {
+        const float2 v = f2_get(f[i / 2]);
+        if (inside(j0 + i)) row[j0 + i] = op_from<T>(v.x);
+        if (inside(j0 + i + 1)) row[j0 + i + 1] = op_from<T>(v.y);
+      }
+    }
+  }
+  // gamma (k = 0) or beta (1) of window w: from shared memory, or (PAR false) from
+  // `q` or, without one, `none`.  Columns that start inside a quad come as the quads
+  // around them, shifted.
+  __device__ __forceinline__ void param(int k, const float* q, float none, int w, F2* f) const {
+    if constexpr (!PAR) {
+      float v[VL];
+      if (q == nullptr) {
+#pragma unroll
+        for (int i = 0; i < VL; ++i) v[i] = none;
+      } else {
+        op_load_f32<VL>(q + col(w), v);
+      }
+#pragma unroll
+      for (int i = 0; i < VL; i += 2) f[i / 2] = f2(v[i], v[i + 1]);
+    } else {
+      // 32 windows on are 32 quads on in either half, or 32 in all (VL = 4)
+      const uint32_t at = static_cast<uint32_t>(k * p.par_floats * 4 + w * 512);
+      float v[VL + 4];
+      op_unpack16<float>(ld_shared16(par[0] + at), v);
+      if constexpr (VL == 8) op_unpack16<float>(ld_shared16(par[1] + at), v + 4);
+      const int o = ALIGNED ? 0 : (NORM_PAD - a) & 3;
+      if (o != 0) {
+        op_unpack16<float>(ld_shared16((VL == 8 ? par[0] + 16 : par[1]) + at), v + VL);
+#pragma unroll
+        for (int i = 0; i < VL; ++i) v[i] = o == 1 ? v[i + 1] : o == 2 ? v[i + 2] : v[i + 3];
+      }
+#pragma unroll
+      for (int i = 0; i < VL; i += 2) f[i / 2] = f2(v[i], v[i + 1]);
+    }
+  }
+};
+
+// NW windows per thread.
+template <typename T, int NW, bool ALIGNED, bool PAR>
+__global__ void __launch_bounds__(NORM_FWD_THREADS, 1) norm_kernel(const NormParams p) {
+  constexpr int VL = kVec<T>, NP = VL / 2;
+  extern __shared__ __align__(128) uint8_t norm_smem[];
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) abort_flag = 0;
+  NormRing<T, 1, NW, ALIGNED, PAR> r(p, norm_smem);
+  __syncthreads();
+  int s = 0, buf = 0;
+  uint32_t phase = 0;
+  uint32_t x = r.mine;
+  T* out = static_cast<T*>(p.out) + r.first * p.H + r.col0;
+  const long long stride = static_cast<long long>(p.walkers) * p.H;
+  for (long long t = r.first; t < p.T; t += p.walkers) {
+    // (a wait that gave up is recorded; the row's results are void)
+    mbar_wait(&r.bars[s], phase, &abort_flag, kFaultNormWait);
+    F2 v[NW][NP];
+    float mean = 0.f;
+    F2 acc = f2(0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (r.col(w) >= p.H) continue;
+      r.load(x, p.x, t, w, 0.f, v[w]);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) acc = f2_add(acc, v[w][i]);
+    }
+    if (!p.rms) {
+      mean = r.sum(f2_sum(acc), buf) * p.inv_h;
+      buf ^= 1;
+    }
+    acc = f2(0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (r.col(w) >= p.H) continue;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        v[w][i] = f2_add(v[w][i], f2(-mean));
+        if (!r.whole(r.col(w))) {  // columns outside the row do not count
+          const float2 e = f2_get(v[w][i]);
+          const int j = r.col(w) + 2 * i;
+          v[w][i] = f2(r.inside(j) ? e.x : 0.f, r.inside(j + 1) ? e.y : 0.f);
+        }
+        acc = f2_fma(v[w][i], v[w][i], acc);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(r.sum(f2_sum(acc), buf) * p.inv_h + p.eps);
+    buf ^= 1;
+    if (r.tid == 0) {
+      // past the last barrier the row is in registers: its stage is filled again
+      const long long ahead = t + static_cast<long long>(p.stages) * p.walkers;
+      if (ahead < p.T) r.issue(ahead, s);
+      if (p.mean != nullptr) p.mean[t] = mean;
+      if (p.rstd != nullptr) p.rstd[t] = rstd;
+    }
+    const F2 rs = f2(rstd);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (r.col(w) >= p.H) continue;
+      F2 m[NP], b[NP];
+      r.param(0, p.gamma, 1.f, w, m);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) v[w][i] = f2_mul(v[w][i], rs);
+      if (p.beta != nullptr) {
+        r.param(1, p.beta, 0.f, w, b);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v[w][i] = f2_fma(v[w][i], m[i], b[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v[w][i] = f2_mul(v[w][i], m[i]);
+      }
+      r.store(out, w, v[w]);
+    }
+    x += r.stage_b;
+    out += stride;
+    if (++s == p.stages) {
+      s = 0;
+      phase ^= 1u;
+      x = r.mine;
     }
   }
 }
 
-// Sum of column c of part[parts][width], in order within each of 32 slices, then
+template <typename T, int NW, bool ALIGNED, bool PAR>
+__global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(const NormParams p) {
+  constexpr int VL = kVec<T>, NP = VL / 2;
+  extern __shared__ __align__(128) uint8_t norm_smem[];
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) abort_flag = 0;
+  NormRing<T, 2, NW, ALIGNED, PAR> r(p, norm_smem);
+  __syncthreads();
+  F2 dg[NW][NP], db[NW][NP];
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+#pragma unroll
+    for (int i = 0; i < NP; ++i) dg[w][i] = db[w][i] = f2(0.f);
+  int s = 0, buf = 0;
+  uint32_t phase = 0;
+  uint32_t x = r.mine;
+  T* out = static_cast<T*>(p.out) + r.first * p.H + r.col0;
+  const long long stride = static_cast<long long>(p.walkers) * p.H;
+  float mean = 0.f, rstd = 0.f;
+  if (r.first < p.T) {
+    mean = p.rms ? 0.f : p.mean[r.first];
+    rstd = p.rstd[r.first];
+  }
+  for (long long t = r.first; t < p.T; t += p.walkers) {
+    float mean_n = 0.f, rstd_n = 0.f;
+    if (t + p.walkers < p.T) {
+      mean_n = p.rms ? 0.f : p.mean[t + p.walkers];
+      rstd_n = p.rstd[t + p.walkers];
+    }
+    // (a wait that gave up is recorded; the row's results are void)
+    mbar_wait(&r.bars[s], phase, &abort_flag, kFaultNormWait);
+    // xh = x rstd - mean rstd; outside the row x = mean, dy = 0
+    const F2 rs = f2(rstd), shift = f2(-mean * rstd);
+    F2 a1 = f2(0.f), a2 = f2(0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (r.col(w) >= p.H) continue;
+      F2 v[NP], d[NP], m[NP];
+      r.load(x, p.x, t, w, mean, v);
+      r.load(x + r.op_b, p.dy, t, w, 0.f, d);
+      r.param(0, p.gamma, 1.f, w, m);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const F2 e = f2_mul(d[i], f2_fma(v[i], rs, shift));
+        dg[w][i] = f2_add(dg[w][i], e);
+        db[w][i] = f2_add(db[w][i], d[i]);
+        a1 = f2_fma(d[i], m[i], a1);
+        a2 = f2_fma(e, m[i], a2);
+      }
+    }
+    float keep = r.sum2_put(f2_sum(a1), f2_sum(a2), buf);
+    r.bar();
+    const float2 sums = r.sum2_get(keep, buf);
+    buf ^= 1;
+    // past this barrier the group is done with the row before: its stage is filled again
+    if (r.tid == 0 && p.stages > 1 && t != r.first) {
+      const long long ahead = t + static_cast<long long>(p.stages - 1) * p.walkers;
+      if (ahead < p.T) r.issue(ahead, s == 0 ? p.stages - 1 : s - 1);
+    }
+    // dx = rstd (dy gamma - s1 - xh s2) = (rstd gamma) dy + k1 x + k0
+    const float s1 = p.rms ? 0.f : sums.x * p.inv_h, s2 = sums.y * p.inv_h;
+    const F2 k1 = f2(-rstd * rstd * s2), k0 = f2(-rstd * fmaf(s2, -mean * rstd, s1));
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (r.col(w) >= p.H) continue;
+      F2 v[NP], d[NP], m[NP];
+      r.load(x, p.x, t, w, mean, v);
+      r.load(x + r.op_b, p.dy, t, w, 0.f, d);
+      r.param(0, p.gamma, 1.f, w, m);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) d[i] = f2_fma(d[i], f2_mul(m[i], rs), f2_fma(v[i], k1, k0));
+      r.store(out, w, d);
+    }
+    if (p.stages == 1) {
+      r.bar();
+      if (r.tid == 0 && t + p.walkers < p.T) r.issue(t + p.walkers, 0);
+    }
+    mean = mean_n;
+    rstd = rstd_n;
+    x += r.stage_b;
+    out += stride;
+    if (++s == p.stages) {
+      s = 0;
+      phase ^= 1u;
+      x = r.mine;
+    }
+  }
+
+  // the groups' sums in group order, by column, in the memory of the rows (every
+  // copy has been waited for)
+  __syncthreads();
+  float* acc = reinterpret_cast<float*>(norm_smem + norm_head(p.groups)) + p.par_floats;
+  for (int g = 0; g < p.groups; ++g) {
+    if (r.g == g) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int i = 0; i < VL; ++i) {
+          const int j = r.col(w) + i;
+          if (!r.inside(j)) continue;
+          const float2 e = f2_get(dg[w][i / 2]), d = f2_get(db[w][i / 2]);
+          const float de = i & 1 ? e.y : e.x, dd = i & 1 ? d.y : d.x;
+          acc[j] = g == 0 ? de : acc[j] + de;
+          acc[p.H + j] = g == 0 ? dd : acc[p.H + j] + dd;
+        }
+    }
+    __syncthreads();
+  }
+  float* part = p.part + static_cast<long long>(blockIdx.x) * 2 * p.H;
+  for (int c = threadIdx.x; c < 2 * p.H; c += blockDim.x) part[c] = acc[c];
+}
+
+// Sum of column c of part[parts][width], in order within each of 16 slices, then
 // over the slices: columns [0, H) go to a_out, the others to b_out (either may
-// be null).
-__global__ void __launch_bounds__(1024)
+// be null).  Four columns a thread where the width allows (W = 4).
+constexpr int COLSUM_SLICES = 16;
+
+template <int W>
+__global__ void __launch_bounds__(32 * COLSUM_SLICES)
     column_sum_kernel(const float* __restrict__ part, int parts, int width, int H, float* __restrict__ a_out,
                       float* __restrict__ b_out) {
-  __shared__ float red[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
-  float a = 0.f;
-  if (c < width)
-    for (int i = threadIdx.y; i < parts; i += 32) a += part[static_cast<long long>(i) * width + c];
-  red[threadIdx.y][threadIdx.x] = a;
+  __shared__ float red[COLSUM_SLICES][32 * W];
+  const int c = (blockIdx.x * 32 + threadIdx.x) * W;
+  float a[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) a[i] = 0.f;
+  if (c < width) {
+#pragma unroll 10
+    for (int k = threadIdx.y; k < parts; k += COLSUM_SLICES) {
+      float v[W];
+      op_load_f32<W>(part + static_cast<long long>(k) * width + c, v);
+#pragma unroll
+      for (int i = 0; i < W; ++i) a[i] += v[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) red[threadIdx.y][threadIdx.x * W + i] = a[i];
   __syncthreads();
-  a = warp_sum(red[threadIdx.x][threadIdx.y]);
-  const int col = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && col < width) {
+  for (int i = threadIdx.y * 32 + threadIdx.x; i < 32 * W; i += 32 * COLSUM_SLICES) {
+    const int col = blockIdx.x * 32 * W + i;
+    if (col >= width) break;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < COLSUM_SLICES; ++k) v += red[k][i];
     if (col < H) {
-      if (a_out != nullptr) a_out[col] = a;
+      if (a_out != nullptr) a_out[col] = v;
     } else if (b_out != nullptr) {
-      b_out[col - H] = a;
+      b_out[col - H] = v;
     }
   }
 }

@@ -31,6 +31,11 @@ void with_type(int t, F f) {
     f(__half());
 }
 
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+
 // ------------------------------------------------------------------------------ routing
 bool route_ok(const moe_route_desc* d) {
   if (d == nullptr || d->T < 0 || d->T > 0x7fffffffLL) return false;
@@ -63,11 +68,6 @@ RouteParams route_params(const moe_route_desc& d) {
 // Calls f(CH, VL as constants) with the fewest loads per lane that hold a row of E
 // elements: 16-byte loads where the rows are made of whole ones, else one element
 // a load.
-template <int V>
-struct Const {
-  static constexpr int value = V;
-};
-
 template <typename T, typename F>
 void route_dispatch(int E, F f) {
   constexpr int V = kVec<T>;
@@ -102,64 +102,112 @@ bool norm_ok(const moe_norm_desc* d) {
          op_type_ok(d->dtype);
 }
 
-// Whether rows of H elements are whole 16-byte vectors.
-bool norm_vec(const moe_norm_desc& d) { return d.H % (16 / op_type_bytes(d.dtype)) == 0; }
-
-template <typename T, int VL>
-void norm_dispatch(const NormParams& p, cudaStream_t s) {
-  const int nvec = p.H / VL;
-  if (nvec <= 128) {
-    const unsigned blocks = static_cast<unsigned>(cdiv(p.T, NORM_WARP_ROWS));
-    const int threads = 32 * NORM_WARP_ROWS;
-    if (nvec <= 32)
-      norm_kernel<T, VL, 1, true><<<blocks, threads, 0, s>>>(p);
-    else if (nvec <= 64)
-      norm_kernel<T, VL, 2, true><<<blocks, threads, 0, s>>>(p);
-    else
-      norm_kernel<T, VL, 4, true><<<blocks, threads, 0, s>>>(p);
-    return;
-  }
-  const unsigned blocks = static_cast<unsigned>(p.T);
-  auto threads = [&](int nv) { return static_cast<int>(cdiv(cdiv(nvec, nv), 32) * 32); };
-  if (nvec <= 1024)
-    norm_kernel<T, VL, 4, false><<<blocks, threads(4), 0, s>>>(p);
-  else if (nvec <= 8192)
-    norm_kernel<T, VL, 8, false><<<blocks, threads(8), 0, s>>>(p);
-  else if constexpr (VL == 1)
-    norm_kernel<T, VL, 16, false><<<blocks, threads(16), 0, s>>>(p);
+// Whether rows of H elements are whole 16-byte windows, and the most windows that
+// a row of them touches.
+bool norm_aligned(const moe_norm_desc& d) { return d.H % (16 / op_type_bytes(d.dtype)) == 0; }
+int norm_windows(const moe_norm_desc& d) {
+  const int vl = 16 / op_type_bytes(d.dtype);
+  return static_cast<int>(norm_aligned(d) ? d.H / vl : cdiv(d.H + vl - 1, vl));
 }
 
-// Blocks of the backward pass: what the parts in the workspace are laid out for.
-int norm_bwd_blocks(const moe_norm_desc& d) {
-  const int vl = norm_vec(d) ? 16 / op_type_bytes(d.dtype) : 1;
-  const long long groups = d.H / vl <= 128 ? 8 : 1;
-  return static_cast<int>(std::max<long long>(1, std::min<long long>(cdiv(d.T, groups), 2LL * num_sms())));
+// How the kernels lay a row length out: nw windows a thread, tpg threads a group,
+// as many groups as the block, the named barriers or the rows allow, and rings as
+// deep as the shared memory is.
+struct NormPlan {
+  int nw, tpg, groups, stages, row_bytes, par_floats, blocks, walkers;
+  size_t smem;
+};
+NormPlan norm_plan(const moe_norm_desc& d, bool backward) {
+  const int vl = 16 / op_type_bytes(d.dtype), windows = norm_windows(d), ops = backward ? 2 : 1;
+  NormPlan q{};
+  const int threads = backward ? NORM_BWD_THREADS : NORM_FWD_THREADS;
+  q.nw = windows <= 32 ? 1 : windows <= 64 ? 2 : windows <= 4 * threads ? 4 : static_cast<int>(cdiv(windows, threads));
+  if (q.nw > 4 && vl == 4 && q.nw < 8) q.nw = 8;  // (fewer variants)
+  q.tpg = static_cast<int>(cdiv(windows, 32 * q.nw) * 32);
+  q.groups = std::max(1, std::min(q.tpg > 32 ? 14 : 32, threads / q.tpg));
+  q.groups = static_cast<int>(std::max<long long>(1, std::min<long long>(q.groups, cdiv(d.T, num_sms()))));
+  q.row_bytes = windows * 16;
+  // gamma and beta in shared memory, unless rows of whole windows are so long that
+  // they would take the ring's place, or so few that no group takes a second one
+  if (!norm_aligned(d) || (d.H <= 8192 && d.T > static_cast<long long>(q.groups) * num_sms()))
+    q.par_floats = static_cast<int>(round_up(d.H + 2 * NORM_PAD, 8));
+  // three stages at least are worth a group
+  for (;; --q.groups) {
+    const size_t head = norm_head(q.groups) + static_cast<size_t>(q.par_floats) * (backward ? 4 : 8);
+    const size_t group = static_cast<size_t>(ops) * q.row_bytes * q.groups;
+    q.stages = static_cast<int>(std::max<size_t>(1, std::min<size_t>(NORM_MAX_RING, (226 * 1024 - head) / group)));
+    q.smem = head + std::max<size_t>(group * q.stages, backward ? static_cast<size_t>(d.H) * 8 : 0);
+    if (q.stages >= 3 || q.groups <= 2) break;
+  }
+  q.blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(cdiv(d.T, q.groups), num_sms())));
+  // rows of one group start at one offset in a window: a stride of whole windows
+  q.walkers = q.blocks * q.groups;
+  if (!norm_aligned(d) && q.walkers < d.T) q.walkers -= q.walkers % vl;
+  return q;
 }
 
-template <typename T, int VL>
-void norm_bwd_dispatch(const NormBwdParams& p, int blocks, cudaStream_t s) {
-  const int nvec = p.H / VL;
-  if (nvec <= 128) {
-    const size_t smem = static_cast<size_t>(p.H) * 8;
-    if (nvec <= 32)
-      norm_backward_kernel<T, VL, 1, true><<<blocks, 256, smem, s>>>(p);
-    else if (nvec <= 64)
-      norm_backward_kernel<T, VL, 2, true><<<blocks, 256, smem, s>>>(p);
-    else
-      norm_backward_kernel<T, VL, 4, true><<<blocks, 256, smem, s>>>(p);
-    return;
+template <typename K>
+moe_status norm_launch(K kern, const NormParams& p, const NormPlan& q, cudaStream_t s) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(q.smem)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  kern<<<q.blocks, q.tpg * q.groups, q.smem, s>>>(p);
+  ++g_last_launches;
+  return launched();
+}
+
+template <typename T, bool ALIGNED, bool PAR, bool BACKWARD>
+moe_status norm_dispatch(const NormParams& p, const NormPlan& q, cudaStream_t s) {
+  auto go = [&](auto nw) {
+    constexpr int NW = decltype(nw)::value;
+    if constexpr (BACKWARD) return norm_launch(norm_backward_kernel<T, NW, ALIGNED, PAR>, p, q, s);
+    else return norm_launch(norm_kernel<T, NW, ALIGNED, PAR>, p, q, s);
+  };
+  // (16-bit rows have at most 2049 windows, fp32 ones 4097)
+  if (q.nw == 1) return go(Const<1>());
+  if (q.nw == 2) return go(Const<2>());
+  if (q.nw == 4) return go(Const<4>());
+  if constexpr (sizeof(T) == 4) {
+    if (q.nw == 8) return go(Const<8>());
+    if constexpr (BACKWARD)
+      if (q.nw == 9) return go(Const<9>());
+  } else if constexpr (BACKWARD) {
+    if (q.nw == 5) return go(Const<5>());
   }
-  auto threads = [&](int nv) { return static_cast<int>(cdiv(cdiv(nvec, nv), 32) * 32); };
-  if (nvec <= 1024)
-    norm_backward_kernel<T, VL, 1, false><<<blocks, threads(1), 0, s>>>(p);
-  else if (nvec <= 2048)
-    norm_backward_kernel<T, VL, 2, false><<<blocks, threads(2), 0, s>>>(p);
-  else if constexpr (VL <= 4) {
-    if (nvec <= 4096)
-      norm_backward_kernel<T, VL, 4, false><<<blocks, threads(4), 0, s>>>(p);
-    else if constexpr (VL == 1)
-      norm_backward_kernel<T, VL, 16, false><<<blocks, threads(16), 0, s>>>(p);
-  }
+  return MOE_ERR_UNSUPPORTED;
+}
+
+template <bool BACKWARD>
+moe_status norm_run(const moe_norm_desc& d, NormParams p, cudaStream_t s) {
+  const NormPlan q = norm_plan(d, BACKWARD);
+  p.T = d.T;
+  p.H = d.H;
+  p.eps = d.eps;
+  p.inv_h = 1.0f / static_cast<float>(d.H);
+  p.rms = d.kind == MOE_NORM_RMS;
+  p.tpg = q.tpg;
+  p.groups = q.groups;
+  p.walkers = q.walkers;
+  p.stages = q.stages;
+  p.row_bytes = q.row_bytes;
+  p.par_floats = q.par_floats;
+  moe_status st = MOE_OK;
+  with_type(d.dtype, [&](auto v) {
+    using T = decltype(v);
+    st = !norm_aligned(d)      ? norm_dispatch<T, false, true, BACKWARD>(p, q, s)
+         : q.par_floats != 0 ? norm_dispatch<T, true, true, BACKWARD>(p, q, s)
+                             : norm_dispatch<T, true, false, BACKWARD>(p, q, s);
+  });
+  return st;
+}
+
+// Column sums of part[parts][width] (see column_sum_kernel).
+void column_sums(const float* part, int parts, int width, int H, float* a_out, float* b_out, cudaStream_t s) {
+  const dim3 block(32, COLSUM_SLICES);
+  if (width % 4 == 0)
+    column_sum_kernel<4><<<static_cast<unsigned>(cdiv(width, 128)), block, 0, s>>>(part, parts, width, H, a_out, b_out);
+  else
+    column_sum_kernel<1><<<static_cast<unsigned>(cdiv(width, 32)), block, 0, s>>>(part, parts, width, H, a_out, b_out);
+  ++g_last_launches;
 }
 
 // ------------------------------------------------------------------------------ linear
@@ -434,23 +482,20 @@ moe_status moe_norm(const moe_norm_desc* d, const void* x, const float* gamma, c
   if (d->T == 0) return MOE_OK;
   if (!ptr_ok(x) || !ptr_ok(y) || !aligned16(gamma) || !aligned16(beta) || !aligned16(mean) || !aligned16(rstd))
     return MOE_ERR_INVALID_ARG;
-  const NormParams p{x, gamma, beta, y, mean, rstd, d->T, d->H, d->eps, 1.0f / d->H, d->kind == MOE_NORM_RMS};
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  with_type(d->dtype, [&](auto v) {
-    using T = decltype(v);
-    if (norm_vec(*d))
-      norm_dispatch<T, kVec<T>>(p, s);
-    else
-      norm_dispatch<T, 1>(p, s);
-  });
-  g_last_launches = 1;
-  return launched();
+  NormParams p{};
+  p.x = x;
+  p.gamma = gamma;
+  p.beta = beta;
+  p.out = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  return norm_run<false>(*d, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moe_norm_backward_workspace_size(const moe_norm_desc* d) {
   using namespace moe;
   if (!norm_ok(d) || d->H > kNormMaxH) return 0;
-  return round_up(static_cast<size_t>(norm_bwd_blocks(*d)) * 2 * d->H * 4, kAlign);
+  return round_up(static_cast<size_t>(norm_plan(*d, true).blocks) * 2 * d->H * 4, kAlign);
 }
 
 moe_status moe_norm_backward(const moe_norm_desc* d, const void* dy, const void* x, const float* gamma,
@@ -467,25 +512,21 @@ moe_status moe_norm_backward(const moe_norm_desc* d, const void* dy, const void*
   if (!ws_fits(ws, ws_bytes, moe_norm_backward_workspace_size(d))) return MOE_ERR_INVALID_ARG;
   g_last_launches = 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int blocks = norm_bwd_blocks(*d);
   float* part = static_cast<float*>(ws);
   if (d->T > 0) {
-    const NormBwdParams p{dy, x, gamma, mean, rstd, dx, part, d->T, d->H, 1.0f / d->H};
-    with_type(d->dtype, [&](auto v) {
-      using T = decltype(v);
-      if (norm_vec(*d))
-        norm_bwd_dispatch<T, kVec<T>>(p, blocks, s);
-      else
-        norm_bwd_dispatch<T, 1>(p, blocks, s);
-    });
-    ++g_last_launches;
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    NormParams p{};
+    p.x = x;
+    p.dy = dy;
+    p.gamma = gamma;
+    p.out = dx;
+    p.mean = const_cast<float*>(mean);
+    p.rstd = const_cast<float*>(rstd);
+    p.part = part;
+    const moe_status st = norm_run<true>(*d, p, s);
+    if (st != MOE_OK) return st;
   }
-  if (dgamma != nullptr || dbeta != nullptr) {
-    column_sum_kernel<<<static_cast<unsigned>(cdiv(2LL * d->H, 32)), dim3(32, 32), 0, s>>>(
-        part, d->T > 0 ? blocks : 0, 2 * d->H, d->H, dgamma, dbeta);
-    ++g_last_launches;
-  }
+  if (dgamma != nullptr || dbeta != nullptr)
+    column_sums(part, d->T > 0 ? norm_plan(*d, true).blocks : 0, 2 * d->H, d->H, dgamma, dbeta, s);
   return launched();
 }
 
@@ -560,11 +601,7 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, const v
     else
       run(__half());
     ++g_last_launches;
-    if (dbias != nullptr) {
-      column_sum_kernel<<<static_cast<unsigned>(cdiv(d->N, 32)), dim3(32, 32), 0, s>>>(
-          part, static_cast<int>(grid.y), d->N, d->N, dbias, nullptr);
-      ++g_last_launches;
-    }
+    if (dbias != nullptr) column_sums(part, static_cast<int>(grid.y), d->N, d->N, dbias, nullptr, s);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     if (act) dp = to;
   }

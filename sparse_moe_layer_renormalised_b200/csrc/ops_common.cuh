@@ -109,6 +109,69 @@ __device__ __forceinline__ void op_load_f32(const float* p, float* f) {
   }
 }
 
+// Two fp32 numbers in a register pair, for the packed arithmetic of sm_100 (one
+// instruction for both, each rounded as the scalar one is).
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
+__device__ __forceinline__ float2 f2_get(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(F2 a) {
+  const float2 r = f2_get(a);
+  return r.x + r.y;
+}
+
+// The 16 bytes q as kVec<T> / 2 pairs, and back.
+template <typename T>
+__device__ __forceinline__ void op_unpack16(const uint4& q, F2* f) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (sizeof(T) == 4) {
+    f[0] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    f[1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = op_unpack(w[i], T());
+      f[i] = f2(p.x, p.y);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 op_pack16(const F2* f) {
+  float g[kVec<T>];
+#pragma unroll
+  for (int i = 0; i < kVec<T> / 2; ++i) {
+    const float2 p = f2_get(f[i]);
+    g[2 * i] = p.x;
+    g[2 * i + 1] = p.y;
+  }
+  return op_pack16<T>(g);
+}
+
 template <typename V>
 __device__ __forceinline__ V warp_sum(V v) {
 #pragma unroll
