@@ -17,7 +17,11 @@
 // linear_wide_kernel: CTA pairs (tcgen05.mma.cta_group::2, 256 x BN tiles, BN a
 // multiple of 32 up to 256), persistent, two accumulators in tensor memory so
 // that a tile's epilogue runs under the next one's products.  For large
-// products; bound by the tensor cores.
+// products; bound by the tensor cores and, close behind, by what the SMs can
+// fetch from L2 (a narrower tile costs nearly as much a k-block as a wide one).
+// The tiles of a last, partly filled wave are split along r over all the pairs;
+// their fp32 partial sums go to the workspace and linear_fixup_kernel adds them
+// up in order and finishes those tiles.
 //
 // linear_skinny_kernel: P on the MMA's 128-row side and at most 128 rows of Q
 // beside it, the sum over r split over the CTAs of a cluster, which add up each
@@ -51,10 +55,28 @@ __host__ __device__ constexpr uint32_t lin_idesc(int M, int N, bool bf16, bool a
 
 enum LinAct : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-// sigmoid by the fast exponential: relative error below 2^-23 (4 + 1.2 |a|).
-__device__ __forceinline__ float lin_sigmoid(float a) { return __fdividef(1.0f, 1.0f + __expf(fminf(-a, 80.f))); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// sigmoid by the fast exponential and reciprocal: relative error below 2^-23 (4 + 1.2 |a|).
+__device__ __forceinline__ float lin_sigmoid(float a) { return rcp_approx(1.0f + __expf(fminf(-a, 80.f))); }
 
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
+
+// erfc(|a| / sqrt 2) as e^(-a^2 / 2) times a polynomial in t = 1 / (1 + 0.3275911 x),
+// x = |a| / sqrt 2 (Abramowitz and Stegun, Handbook of Mathematical Functions,
+// 7.1.26; absolute error 1.5e-7): a third of erff's instructions, and no branch.
+// *e receives the exponential.
+__device__ __forceinline__ float lin_erfc_abs(float a, float* e) {
+  const float x = fabsf(a) * 0.7071067811865476f;
+  const float t = rcp_approx(fmaf(0.3275911f, x, 1.0f));
+  *e = __expf(-x * x);
+  const float q = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t, 0.254829592f);
+  return q * t * *e;
+}
 
 __device__ __forceinline__ float lin_act(float a, int act) {
   switch (act) {
@@ -62,8 +84,12 @@ __device__ __forceinline__ float lin_act(float a, int act) {
       return a > 0.f ? a : (a == a ? 0.f : a);
     case kActSilu:
       return a * lin_sigmoid(a);
-    case kActGelu:
-      return 0.5f * a * (1.0f + erff(a * 0.7071067811865476f));
+    case kActGelu: {
+      // a Phi(a) = max(a, 0) - |a| erfc(|a| / sqrt 2) / 2 on both sides of 0
+      float e;
+      const float c = lin_erfc_abs(a, &e);
+      return a == a ? fmaf(-0.5f * fabsf(a), c, fmaxf(a, 0.f)) : a;
+    }
     case kActGeluTanh:  // (1 + tanh u) / 2 = sigmoid(2 u)
       return a * lin_sigmoid(2.f * kSqrt2OverPi * (a + 0.044715f * a * a * a));
     default:
@@ -79,8 +105,11 @@ __device__ __forceinline__ float lin_act_grad(float a, int act) {
       const float s = lin_sigmoid(a);
       return s * (1.0f + a * (1.0f - s));
     }
-    case kActGelu:
-      return 0.5f * (1.0f + erff(a * 0.7071067811865476f)) + a * 0.3989422804014327f * __expf(-0.5f * a * a);
+    case kActGelu: {
+      float e;
+      const float c = 0.5f * lin_erfc_abs(a, &e);
+      return (a > 0.f ? 1.0f - c : c) + a * 0.3989422804014327f * e;
+    }
     case kActGeluTanh: {
       const float s = lin_sigmoid(2.f * kSqrt2OverPi * (a + 0.044715f * a * a * a));
       return s + a * 2.f * s * (1.f - s) * kSqrt2OverPi * (1.f + 3.f * 0.044715f * a * a);
@@ -92,6 +121,8 @@ __device__ __forceinline__ float lin_act_grad(float a, int act) {
 
 struct LinMaps {
   CUtensorMap p, q;
+  // wide, 16-bit outputs: boxes of 32 x 32 of out, residual and pre
+  CUtensorMap out, res, pre;
 };
 
 struct LinParams {
@@ -106,6 +137,10 @@ struct LinParams {
   void* out;
   int act;
   int fault_site;
+  // wide: the first `full` tiles whole, each later one in `split` parts, whose sums go
+  // to partial[part][bn / 4][256][4]
+  int full, split;
+  float* partial;
 };
 
 // bias, pre, activation and residual of NC consecutive outputs of a row (NC a
@@ -171,11 +206,45 @@ __device__ __forceinline__ void lin_finish(const LinParams& p, long long q, int 
 }
 
 // ------------------------------------------------------------------------------ wide
-constexpr int LW_STAGES = 6;
+constexpr int LW_STAGES = 5;
 constexpr uint32_t LW_OPER_BYTES = 128 * LIN_BK * 2;  // one operand's stage in a CTA
 constexpr int LW_THREADS = 32 * 10;
-constexpr size_t LW_SMEM = 1024 + static_cast<size_t>(LW_STAGES) * 2 * LW_OPER_BYTES + 256;
-constexpr int LW_GROUP = 8;  // Q tiles that share a run of P tiles through L2
+// An epilogue warp's boxes of 32 x 32 16-bit values: two for out (and the residual
+// in its place), two for pre.
+constexpr uint32_t LW_BOX = 32 * 32 * 2;
+constexpr uint32_t LW_WARP_BYTES = 4 * LW_BOX;
+constexpr size_t LW_SMEM = 1024 + static_cast<size_t>(LW_STAGES) * 2 * LW_OPER_BYTES + 8 * LW_WARP_BYTES + 512;
+constexpr int LW_GROUP = 16;  // Q tiles that share a run of P tiles through L2
+
+// Store of a box from shared memory; parts outside the tensor are left out.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+// The activation of 32 values, chosen once.
+__device__ __forceinline__ void lin_act32(float (&a)[32], int act) {
+  switch (act) {
+    case kActNone:
+      break;
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) a[i] = lin_act(a[i], kActRelu);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) a[i] = lin_act(a[i], kActSilu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) a[i] = lin_act(a[i], kActGelu);
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) a[i] = lin_act(a[i], kActGeluTanh);
+  }
+}
 
 struct LinTile {
   int q, p;
@@ -191,6 +260,18 @@ __device__ __forceinline__ LinTile lw_tile(int w, const LinParams& p) {
   return {grp * LW_GROUP + (r - pt * rows), pt};
 }
 
+// Work item w: a tile and its k-blocks [kb0, kb1); part < 0: all of them.
+struct LinItem {
+  LinTile t;
+  int kb0, kb1, part;
+};
+__device__ __forceinline__ LinItem lw_item(int w, const LinParams& p) {
+  if (w < p.full) return {lw_tile(w, p), 0, p.nkb, -1};
+  const int i = w - p.full, tile = i / p.split, k = i - tile * p.split;
+  return {lw_tile(p.full + tile, p), static_cast<int>(static_cast<long long>(p.nkb) * k / p.split),
+          static_cast<int>(static_cast<long long>(p.nkb) * (k + 1) / p.split), i};
+}
+
 template <typename OutT>
 __global__ void __launch_bounds__(LW_THREADS, 1)
     linear_wide_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
@@ -198,12 +279,14 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lw_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;                                // Q rows
   uint8_t* sB = smem + LW_STAGES * LW_OPER_BYTES;    // P rows
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + LW_STAGES * LW_OPER_BYTES);
+  uint8_t* sE = sB + LW_STAGES * LW_OPER_BYTES;      // the epilogue warps' boxes
+  uint64_t* full = reinterpret_cast<uint64_t*>(sE + 8 * LW_WARP_BYTES);
   uint64_t* empty = full + LW_STAGES;
   uint64_t* acc_full = empty + LW_STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* res_full = drain + 1;                    // [8 warps][2]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(res_full + 16);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -211,7 +294,7 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int total = p.q_tiles * p.p_tiles;
+  const int total = p.full + (p.q_tiles * p.p_tiles - p.full) * p.split;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < LW_STAGES; ++s) {
@@ -222,6 +305,7 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], 16);  // the eight epilogue warps of both CTAs
     }
+    for (int i = 0; i < 16; ++i) mbar_init(&res_full[i], 1);
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
@@ -247,10 +331,10 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
       const int p_boxes = (half + 63) >> 6;
       const uint32_t bytes = 2u * (LW_OPER_BYTES + (p.p_mn ? p_boxes * LIN_BOX_MN : static_cast<uint32_t>(half) * 128u));
       for (int w = pair; w < total && ok; w += npairs) {
-        const LinTile t = lw_tile(w, p);
-        const int q0 = t.q * 256 + static_cast<int>(rank) * 128;
-        const int p0 = t.p * p.bn + static_cast<int>(rank) * half;
-        for (int kb = 0; kb < p.nkb; ++kb) {
+        const LinItem it = lw_item(w, p);
+        const int q0 = it.t.q * 256 + static_cast<int>(rank) * 128;
+        const int p0 = it.t.p * p.bn + static_cast<int>(rank) * half;
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort, p.fault_site + 1)) {
             ok = false;
             break;
@@ -299,10 +383,11 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
       uint32_t acc_phase = 0;
       bool ok = true;
       for (int w = pair; w < total && ok; w += npairs) {
+        const LinItem it = lw_item(w, p);
         if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, abort, p.fault_site + 3)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-        for (int kb = 0; kb < p.nkb; ++kb) {
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
           if (!mbar_wait(&full[stage], phase, abort, p.fault_site + 4)) {
             ok = false;
             break;
@@ -314,7 +399,8 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
           const uint64_t bd = p.p_mn ? sw128_mnmajor_desc(b_addr) : sw128_kmajor_desc(b_addr);
 #pragma unroll
           for (int kk = 0; kk < LIN_BK / 16; ++kk)
-            ex_mma<2>(d_tmem, ad + ((kk * a_step) >> 4), bd + ((kk * b_step) >> 4), idesc, (kb | kk) != 0 ? 1u : 0u);
+            ex_mma<2>(d_tmem, ad + ((kk * a_step) >> 4), bd + ((kk * b_step) >> 4), idesc,
+                      kb != it.kb0 || kk != 0 ? 1u : 0u);
           ex_commit<2>(&empty[stage]);
           if (++stage == LW_STAGES) {
             stage = 0;
@@ -344,20 +430,120 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
     const uint32_t acc_empty_leader = map_to_rank(smem_u32(&acc_empty[0]), 0u);
     int acc = 0;
     uint32_t acc_phase = 0;
+    // 16-bit outputs go through shared memory and TMA, 32 x 32 at a time, the
+    // residual's box loaded one chunk ahead into the place of the output's
+    // (straight from registers each lane writes a row of its own: 32 lines an
+    // access, and a sixth of the whole kernel's time at 8192 x 7168 x 3584)
+    constexpr bool kBoxes = sizeof(OutT) == 2;
+    uint8_t* boxes = sE + (warp - 2) * LW_WARP_BYTES;
+    uint64_t* res_bar = res_full + (warp - 2) * 2;
+    const bool has_res = p.residual != nullptr, has_pre = p.pre != nullptr;
+    int n = 0, ahead = 0;  // chunks done by this warp, residual boxes asked for
+    int w_next = pair, c_next = set * 32;  // the next chunk to load a residual for
+    auto chunk_row = [&](int w) { return lw_tile(w, p).q * 256 + static_cast<int>(rank) * 128 + quarter * 32; };
+    // moves (w, c) to the first chunk at or after it that this warp has rows and columns in
+    auto settle = [&](int& w, int& c) {
+      for (; w < p.full; w += npairs, c = set * 32) {  // (parts have no residual)
+        const LinTile t = lw_tile(w, p);
+        if (c < p.bn && t.p * p.bn + c < p.P && chunk_row(w) < p.Q) return;
+      }
+    };
+    auto load_res = [&](int slot) {  // one lane
+      const LinTile t = lw_tile(w_next, p);
+      mbar_arrive_expect_tx(&res_bar[slot], LW_BOX);
+      tma_load_2d(boxes + slot * LW_BOX, &maps.res, &res_bar[slot], t.p * p.bn + c_next, chunk_row(w_next));
+    };
+    if (kBoxes && has_res) {
+      settle(w_next, c_next);
+      if (w_next < p.full) {
+        if (lane == 0) load_res(0);
+        ++ahead;
+        c_next += 64;
+        settle(w_next, c_next);
+      }
+    }
     for (int w = pair; w < total; w += npairs) {
-      const LinTile t = lw_tile(w, p);
+      const LinItem it = lw_item(w, p);
+      const LinTile t = it.t;
       // warp-uniform decision: tcgen05.ld below needs the whole warp
       if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase, abort, p.fault_site + 6))) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * 256);
-      const long long q = static_cast<long long>(t.q) * 256 + rank * 128 + quarter * 32 + lane;
+      const int row0 = t.q * 256 + static_cast<int>(rank) * 128 + quarter * 32;
+      const long long q = static_cast<long long>(row0) + lane;
 #pragma unroll 1
       for (int c = set * 32; c < p.bn; c += 64) {
         const int col = t.p * p.bn + c;
         if (col >= p.P) break;  // warp-uniform
         float a[32];
         tmem_ld32(tbase + c, a);
-        if (q < p.Q) {
+        if (it.part >= 0) {
+          // lanes (rows) beside one another, four columns each
+          float4* to = reinterpret_cast<float4*>(p.partial) + static_cast<long long>(it.part) * (p.bn / 4) * 256 +
+                       (c / 4) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) to[i * 256] = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+        } else if constexpr (kBoxes) {
+          if (row0 < p.Q) {  // warp-uniform
+            const int slot = n & 1;
+            if (lane == 0) {
+              // the box of the chunk before last has been written out; with a residual
+              // also the last one's, whose place the next residual takes
+              if (has_res) {
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                if (w_next < p.full) load_res(slot ^ 1);
+              } else {
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+              }
+            }
+            if (has_res && w_next < p.full) {
+              ++ahead;
+              c_next += 64;
+              settle(w_next, c_next);
+            }
+            __syncwarp();
+            if (has_res) mbar_wait(&res_bar[slot], (n >> 1) & 1, abort, p.fault_site + 7);
+            uint8_t* box = boxes + slot * LW_BOX + lane * 64;
+            const int swz = (lane >> 1) & 3;  // 64-byte swizzle: 16-byte word j of row r at j ^ (r / 2 % 4)
+            if (p.bias != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                if (col + i < p.P) {
+                  const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col + i));
+                  a[i] += b.x;
+                  a[i + 1] += b.y;
+                  a[i + 2] += b.z;
+                  a[i + 3] += b.w;
+                }
+              }
+            }
+            if (has_pre) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(box + 2 * LW_BOX + ((j ^ swz) << 4)) = op_pack16<OutT>(a + 8 * j);
+            }
+            lin_act32(a, p.act);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint4* at = reinterpret_cast<uint4*>(box + ((j ^ swz) << 4));
+              if (has_res) {
+                float r[8];
+                op_unpack16<OutT>(*at, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[8 * j + i] += r[i];
+              }
+              *at = op_pack16<OutT>(a + 8 * j);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&maps.out, boxes + slot * LW_BOX, col, row0);
+              if (has_pre) tma_store_2d(&maps.pre, boxes + (2 + slot) * LW_BOX, col, row0);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            ++n;
+          }
+        } else if (q < p.Q) {
           if (col + 32 <= p.P) {
             lin_finish<OutT, 32>(p, q, col, a);
           } else {
@@ -377,6 +563,13 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
         acc_phase ^= 1u;
       }
     }
+    // the stores have read their boxes, and (after a wait that gave up) a residual's
+    // has landed, before the memory goes
+    if (ahead > n) {
+      volatile int never = 0;
+      mbar_wait(&res_bar[n & 1], (n >> 1) & 1, &never, p.fault_site + 8);
+    }
+    if (kBoxes && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   __syncwarp();  // reconverge lanes that skipped the single-thread roles
@@ -387,6 +580,29 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
     __syncwarp();
     ex_tmem_dealloc<2>(tmem_base);
   }
+}
+
+// The tiles that linear_wide_kernel left in parts: four columns of a row a thread,
+// the parts added in order.
+template <typename OutT>
+__global__ void __launch_bounds__(256) linear_fixup_kernel(const LinParams p) {
+  const int quads = p.bn / 4;
+  const int tile = blockIdx.x / quads, cq = blockIdx.x - tile * quads, row = threadIdx.x;
+  const LinTile t = lw_tile(p.full + tile, p);
+  const long long q = static_cast<long long>(t.q) * 256 + row;
+  const int col = t.p * p.bn + cq * 4;
+  if (q >= p.Q || col >= p.P) return;
+  const float4* from = reinterpret_cast<const float4*>(p.partial) + (static_cast<long long>(tile) * p.split * quads + cq) * 256 + row;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int k = 0; k < p.split; ++k) {
+    const float4 v = from[static_cast<long long>(k) * quads * 256];
+    a[0] += v.x;
+    a[1] += v.y;
+    a[2] += v.z;
+    a[3] += v.w;
+  }
+  lin_finish<OutT, 4>(p, q, col, a);
 }
 
 // ------------------------------------------------------------------------------ skinny
@@ -549,13 +765,18 @@ __global__ void __launch_bounds__(LS_THREADS, 2)
   for (int i = rank * LS_THREADS + threadIdx.x; i < BN * 32; i += split * LS_THREADS) {
     const int row = i >> 5, col = p0 + (i & 31) * 4;
     if (q0 + row >= p.Q || col >= p.P) continue;
+    float4 v[LS_MAX_SPLIT];
+#pragma unroll
+    for (int s = 0; s < LS_MAX_SPLIT; ++s)
+      v[s] = s < split ? ld_cluster_f4(map_to_rank(part_addr + static_cast<uint32_t>(i) * 16u, static_cast<uint32_t>(s)))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
     float a[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < split; ++s) {
-      const float4 v = ld_cluster_f4(map_to_rank(part_addr + static_cast<uint32_t>(i) * 16u, static_cast<uint32_t>(s)));
-      a[0] += v.x;
-      a[1] += v.y;
-      a[2] += v.z;
-      a[3] += v.w;
+#pragma unroll
+    for (int s = 0; s < LS_MAX_SPLIT; ++s) {
+      a[0] += v[s].x;
+      a[1] += v[s].y;
+      a[2] += v[s].z;
+      a[3] += v[s].w;
     }
     lin_finish<OutT, 4>(p, q0 + row, col, a);
   }

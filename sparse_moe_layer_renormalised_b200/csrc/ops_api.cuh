@@ -232,19 +232,59 @@ bool lin_map(CUtensorMap* m, const void* base, bool mn, long long rows, long lon
   return mn ? make_map(m, base, R, rows, rows, LIN_BK) : make_map(m, base, rows, R, R, box_rows);
 }
 
-// Tile width of the wide kernel: the widest of those that give the shortest
-// last wave (a tile costs its width and about 32 columns' time besides).
-int lin_wide_bn(long long q_tiles, long long P, int pairs) {
-  int best = 256;
+// Boxes of 32 x 32 16-bit values of a [Q, P] matrix, 64-byte swizzle.
+bool lin_box_map(CUtensorMap* m, const void* base, long long Q, long long P) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(P), static_cast<cuuint64_t>(Q)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(P) * 2};
+  cuuint32_t box[2] = {32, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tiles of the wide kernel: their width, how many are done whole, and in how many
+// parts each of the others.
+struct LinWidePlan {
+  int bn, p_tiles, q_tiles, full, split;
+  long long items() const { return full + (static_cast<long long>(p_tiles) * q_tiles - full) * split; }
+};
+
+// The width with the least time by this count: a tile's k-block costs about as the
+// 256 + bn operand rows that are fetched for it (measured at 8192 x 7168 x 3584 and
+// 4001 x 3584 x 7168 with widths of 160 to 256); full waves cost one tile each, a
+// last one that is split into s parts 1 / s and a little more.
+LinWidePlan lin_wide_plan(long long Q, long long P, int nkb, int pairs) {
+  LinWidePlan best{};
   double cost = 0.0;
   for (int bn = 256; bn >= 128; bn -= 32) {
-    const double c = static_cast<double>(cdiv(q_tiles * cdiv(P, bn), pairs)) * (bn + 32);
-    if (bn == 256 || c < cost) {
-      best = bn;
+    LinWidePlan w{};
+    w.bn = bn;
+    w.q_tiles = static_cast<int>(cdiv(Q, 256));
+    w.p_tiles = static_cast<int>(cdiv(P, bn));
+    const long long tiles = static_cast<long long>(w.q_tiles) * w.p_tiles, waves = tiles / pairs, rest = tiles - waves * pairs;
+    w.split = 1;
+    // parts of eight k-blocks at least
+    if (rest > 0) w.split = static_cast<int>(std::max<long long>(1, std::min<long long>(pairs / rest, nkb / 8)));
+    w.full = static_cast<int>(w.split > 1 ? waves * pairs : tiles);
+    const double c = (waves + (rest == 0 ? 0.0 : w.split > 1 ? 1.0 / w.split + 0.1 : 1.0)) * (256 + bn);
+    if (best.bn == 0 || c < cost) {
+      best = w;
       cost = c;
     }
   }
   return best;
+}
+
+// Bytes for the partial sums of a last wave, whatever the plan: one tile a pair.
+size_t lin_wide_ws() { return static_cast<size_t>(num_sms() / 2) * 256 * 256 * 4; }
+
+// Few rows, or fewer tiles than would keep half the pairs at work even in parts:
+// the skinny kernel.
+bool lin_is_skinny(long long Q, long long P) {
+  return Q <= 128 || cdiv(Q, 256) * cdiv(P, 256) < 8;
 }
 
 template <typename OutT>
@@ -265,15 +305,31 @@ cudaError_t lin_launch_wide(const LinProblem& g, LinParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   static int pairs_cache[128] = {};
   const int pairs = cluster_pairs(kern, cfg, pairs_cache);
-  const long long q_tiles = cdiv(g.Q, 256);
-  p.bn = lin_wide_bn(q_tiles, g.P, pairs);
-  p.q_tiles = static_cast<int>(q_tiles);
-  p.p_tiles = static_cast<int>(cdiv(g.P, p.bn));
+  const LinWidePlan w = lin_wide_plan(g.Q, g.P, p.nkb, std::min(pairs, num_sms() / 2));
+  p.bn = w.bn;
+  p.q_tiles = w.q_tiles;
+  p.p_tiles = w.p_tiles;
+  p.full = w.full;
+  p.split = w.split;
   LinMaps maps;
+  std::memset(&maps, 0, sizeof maps);
   if (!lin_map(&maps.p, g.p, g.p_mn, g.P, g.R, p.bn / 2) || !lin_map(&maps.q, g.q, g.q_mn, g.Q, g.R, 128))
     return cudaErrorInvalidValue;
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(pairs, q_tiles * p.p_tiles)));
-  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+  if (sizeof(OutT) == 2) {
+    if (!lin_box_map(&maps.out, p.out, g.Q, g.P) || (p.residual != nullptr && !lin_box_map(&maps.res, p.residual, g.Q, g.P)) ||
+        (p.pre != nullptr && !lin_box_map(&maps.pre, p.pre, g.Q, g.P)))
+      return cudaErrorInvalidValue;
+  }
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(pairs, w.items())));
+  e = cudaLaunchKernelEx(&cfg, kern, maps, p);
+  ++g_last_launches;
+  const long long rest = static_cast<long long>(w.p_tiles) * w.q_tiles - w.full;
+  if (e == cudaSuccess && rest > 0) {
+    linear_fixup_kernel<OutT><<<static_cast<unsigned>(rest * (w.bn / 4)), 256, 0, s>>>(p);
+    ++g_last_launches;
+    e = cudaGetLastError();
+  }
+  return e;
 }
 
 template <typename OutT, int BN>
@@ -290,6 +346,7 @@ cudaError_t lin_launch_skinny(const LinProblem& g, LinParams& p, cudaStream_t s)
   const int split = static_cast<int>(
       std::max<long long>(1, std::min<long long>({LS_MAX_SPLIT, 2LL * num_sms() / tiles, p.nkb / 2})));
   LinMaps maps;
+  std::memset(&maps, 0, sizeof maps);
   if (!lin_map(&maps.p, g.p, g.p_mn, g.P, g.R, 128) || !lin_map(&maps.q, g.q, g.q_mn, g.Q, g.R, BN))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -314,19 +371,17 @@ moe_status lin_product(const LinProblem& g, LinParams p, cudaStream_t s) {
   p.nkb = static_cast<int>(cdiv(g.R, LIN_BK));
   p.p_mn = g.p_mn;
   p.q_mn = g.q_mn;
-  const long long wide = cdiv(g.Q, 256) * cdiv(g.P, 256);
   if (cdiv(g.Q, 256) * cdiv(g.P, 128) > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   cudaError_t e;
-  // few rows, or fewer than half the CTA pairs at work on 256 x 256 tiles
-  if (g.Q <= 128 || wide < num_sms() / 4) {
+  if (lin_is_skinny(g.Q, g.P)) {
     e = g.Q <= 16   ? lin_launch_skinny<OutT, 16>(g, p, s)
         : g.Q <= 32 ? lin_launch_skinny<OutT, 32>(g, p, s)
         : g.Q <= 64 ? lin_launch_skinny<OutT, 64>(g, p, s)
                     : lin_launch_skinny<OutT, 128>(g, p, s);
+    ++g_last_launches;
   } else {
     e = lin_launch_wide<OutT>(g, p, s);
   }
-  ++g_last_launches;
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -531,21 +586,21 @@ moe_status moe_norm_backward(const moe_norm_desc* d, const void* dy, const void*
 }
 
 size_t moe_linear_workspace_size(const moe_linear_desc* d) {
-  (void)d;
-  return 0;  // split sums meet in the CTAs' shared memory
+  using namespace moe;
+  if (lin_check(d) != MOE_OK) return 0;
+  return lin_is_skinny(d->M, d->N) ? 0 : lin_wide_ws();
 }
 
 moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* weight, const float* bias,
                       const void* residual, void* pre, void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
   using namespace moe;
-  (void)ws;
-  (void)ws_bytes;
   moe_status st = lin_check(d);
   if (st != MOE_OK) return st;
   g_last_launches = 0;
   if (d->M == 0) return MOE_OK;
   if (!ptr_ok(x) || !ptr_ok(weight) || !ptr_ok(y) || !aligned16(bias) || !aligned16(residual) || !aligned16(pre))
     return MOE_ERR_INVALID_ARG;
+  if (!ws_fits(ws, ws_bytes, moe_linear_workspace_size(d))) return MOE_ERR_INVALID_ARG;
   LinParams p{};
   p.bf16 = d->dtype == MOE_BF16;
   p.bias = bias;
@@ -554,6 +609,7 @@ moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* weigh
   p.out = y;
   p.act = d->act;
   p.fault_site = 200;
+  p.partial = static_cast<float*>(ws);
   const LinProblem g{weight, x, false, false, d->N, d->M, d->K};
   return lin_product_of(d->y_out, g, p, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -561,7 +617,7 @@ moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* weigh
 size_t moe_linear_backward_workspace_size(const moe_linear_desc* d) {
   using namespace moe;
   if (lin_check(d) != MOE_OK) return 0;
-  return lin_dp_bytes(*d) + round_up(static_cast<size_t>(lin_dp_parts(*d)) * d->N * 4, kAlign);
+  return lin_dp_bytes(*d) + round_up(static_cast<size_t>(lin_dp_parts(*d)) * d->N * 4, kAlign) + lin_wide_ws();
 }
 
 moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, const void* pre, const void* x,
@@ -608,6 +664,7 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, const v
   LinParams p{};
   p.bf16 = d->dtype == MOE_BF16;
   p.act = kActNone;
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + moe_linear_backward_workspace_size(d) - lin_wide_ws());
   if (dx != nullptr) {
     p.out = dx;
     p.fault_site = 210;

@@ -13,7 +13,7 @@ ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
 # the smallest, one tile and its ragged edges, few rows with a split sum, and large enough for the wide tiles
 SHAPES = [(1, 8, 8), (3, 16, 40), (5, 72, 136), (16, 128, 64), (17, 256, 200), (1, 1000, 3584), (4, 7168, 512), (33, 136, 1000),
           (64, 512, 512), (65, 384, 72), (128, 1032, 264), (129, 640, 264), (200, 1000, 328), (256, 2048, 512),
-          (1111, 2048, 1024), (2049, 2312, 520), (4100, 3592, 136), (300, 8200, 1032)]
+          (1111, 2048, 1024), (2049, 2312, 520), (4100, 3592, 136), (300, 8200, 1032), (520, 2304, 2112), (2048, 7168, 640), (2304, 8456, 1096)]
 
 
 def _accumulation(R):
@@ -27,6 +27,10 @@ def _data(M, N, K, dtype, seed):
     return r(M, K).to(DT[dtype]), (r(N, K) * K ** -0.5).to(DT[dtype]), r(N) * 0.2, r(M, N)
 
 
+def _linear(d, *args):
+    return moe.moe_linear(d, *args, workspace(moe.moe_linear_workspace_size(d)))
+
+
 def _check(M, N, K, dtype, act, y_out=None, bias=True, residual=True, pre=True, inplace=False):
     y_out = y_out or dtype
     x, w, b, res = _data(M, N, K, dtype, M + 3 * N + K)
@@ -38,7 +42,7 @@ def _check(M, N, K, dtype, act, y_out=None, bias=True, residual=True, pre=True, 
     pd = g.new((M, N), DT[dtype]) if pre else None
     y = rd if inplace else g.new((M, N), DT[y_out])
     d = moe.linear_desc(M, N, K, act, dtype, y_out)
-    assert moe.moe_linear(d, xd, wd, bd, rd, pd, y) == moe.MOE_OK
+    assert _linear(d, xd, wd, bd, rd, pd, y) == moe.MOE_OK
     g.check()
     want_pre, want = oo.linear(x, w, b if bias else None, res if residual else None, act)
     size = x.double().abs() @ w.double().abs().T
@@ -79,7 +83,7 @@ def test_non_finite_rows_stay_alone():
     x[3, 100] = math.inf
     x[9, 5] = math.nan
     y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
-    assert moe.moe_linear(moe.linear_desc(M, N, K), x, w, None, None, None, y) == moe.MOE_OK
+    assert _linear(moe.linear_desc(M, N, K), x, w, None, None, None, y) == moe.MOE_OK
     bad = ~torch.isfinite(y).all(1).cpu()
     assert bad.nonzero().view(-1).tolist() == [3, 9]
 
@@ -154,12 +158,12 @@ def test_gradients_against_differences():
 
     def loss(x, w):
         y = torch.empty(M, N, device="cuda")
-        assert moe.moe_linear(d32, x, w, None, None, None, y) == moe.MOE_OK
+        assert _linear(d32, x, w, None, None, None, y) == moe.MOE_OK
         return float((y.double() * dy.double()).sum())
 
     pre = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
     y = torch.empty(M, N, device="cuda")
-    assert moe.moe_linear(d32, x, w, None, None, pre, y) == moe.MOE_OK
+    assert _linear(d32, x, w, None, None, pre, y) == moe.MOE_OK
     d = moe.linear_desc(M, N, K, "silu")
     dx, dw = torch.empty_like(x), torch.empty_like(w)
     ws = workspace(moe.moe_linear_backward_workspace_size(d))
@@ -184,6 +188,6 @@ def test_deterministic():
         outs = []
         for _ in range(3):
             y = torch.empty(M, 2048, dtype=torch.bfloat16, device="cuda")
-            assert moe.moe_linear(moe.linear_desc(M, 2048, 2048, "gelu"), x, w, b, res, None, y) == moe.MOE_OK
+            assert _linear(moe.linear_desc(M, 2048, 2048, "gelu"), x, w, b, res, None, y) == moe.MOE_OK
             outs.append(y.cpu())
         assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])

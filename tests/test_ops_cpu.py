@@ -118,6 +118,11 @@ def test_linear_refuses():
     assert moe.moe_linear_backward(d, *good, FAKE, n - 1, 0) == BAD
     assert moe.moe_linear_backward(d, *good, FAKE + 16, n, 0) == BAD
     assert moe.moe_linear_backward(d, *good, None, n, 0) == BAD
+    big = moe.linear_desc(4096, 4096, 64)
+    n = moe.moe_linear_workspace_size(big)
+    assert n > 0 and moe.moe_linear_workspace_size(d) == 0
+    for ws, size in ((None, n), (FAKE, n - 1), (FAKE + 16, n)):
+        assert moe.moe_linear(big, *ptrs, ws, size, 0) == BAD
     assert moe.moe_linear(moe.linear_desc(0, 64, 64), None, None, None, None, None, None, None, None, 0) == moe.MOE_OK
 
 
