@@ -118,6 +118,8 @@ template <int MAXT, bool MAX>
 __global__ void __launch_bounds__(CLIP_THREADS)
     clip_norm_kernel(const __grid_constant__ ClipList<MAXT> l, double* __restrict__ partial) {
   __shared__ double red[CLIP_THREADS / 32];
+  pdl_next();
+  pdl_wait();
   double sum = 0.0;
   uint32_t top = 0u;
   for (int c = blockIdx.x; c < l.chunks; c += gridDim.x) {
@@ -190,6 +192,8 @@ __global__ void __launch_bounds__(CLIP_THREADS)
                       float max_norm, float* __restrict__ norm_out) {
   __shared__ double red[CLIP_THREADS / 32];
   __shared__ float s_coef;
+  pdl_next();
+  pdl_wait();
   // every block forms the same norm, in the same order
   double a = 0.0;
   for (int i = threadIdx.x; i < parts; i += CLIP_THREADS) {

@@ -318,6 +318,8 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
+  pdl_next();
+  pdl_wait();
   const uint32_t tmem_base = *tmem_holder;
   const int half = p.bn >> 1;  // P rows that this CTA stages
 
@@ -586,6 +588,8 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
 // the parts added in order.
 template <typename OutT>
 __global__ void __launch_bounds__(256) linear_fixup_kernel(const LinParams p) {
+  pdl_next();
+  pdl_wait();
   const int quads = p.bn / 4;
   const int tile = blockIdx.x / quads, cq = blockIdx.x - tile * quads, row = threadIdx.x;
   const LinTile t = lw_tile(p.full + tile, p);
@@ -610,12 +614,11 @@ constexpr int LS_THREADS = 192;
 constexpr uint32_t LS_BUDGET = 108 * 1024;  // operand stages: two CTAs an SM
 constexpr int LS_MAX_SPLIT = 8;
 
-// BN rows of Q a tile.
-template <int BN>
+// BN rows of Q a tile; an MN-major Q takes whole boxes of 64 rows.
+template <int BN, bool QMN>
 struct LsCfg {
   static constexpr uint32_t kP = 128 * LIN_BK * 2;
-  // an MN-major Q takes whole boxes of 64 rows
-  static constexpr uint32_t kQ = (BN < 64 ? 64 : BN) * LIN_BK * 2;
+  static constexpr uint32_t kQ = (QMN && BN < 64 ? 64 : BN) * LIN_BK * 2;
   static constexpr uint32_t kStage = kP + kQ;
   static constexpr int kStages = LS_BUDGET / kStage > 8 ? 8 : static_cast<int>(LS_BUDGET / kStage);
   static constexpr uint32_t kCols = BN < 32 ? 32 : BN;  // tensor memory columns
@@ -629,10 +632,10 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-template <typename OutT, int BN>
+template <typename OutT, int BN, bool QMN>
 __global__ void __launch_bounds__(LS_THREADS, 2)
     linear_skinny_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
-  using C = LsCfg<BN>;
+  using C = LsCfg<BN, QMN>;
   extern __shared__ uint8_t ls_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ls_smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage);
@@ -655,11 +658,11 @@ __global__ void __launch_bounds__(LS_THREADS, 2)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    tma_prefetch_desc(&maps.p);
+    tma_prefetch_desc(&maps.q);
     mbar_init(done, 1);
     *abort = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&maps.p);
-    tma_prefetch_desc(&maps.q);
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, C::kCols);
@@ -668,6 +671,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_next();
+  pdl_wait();
   const uint32_t tmem_base = *tmem_holder;
 
   if (warp == 0) {
@@ -675,7 +680,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2)
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued = 0u, issued_parity = 0u;
-      const uint32_t bytes = C::kP + (p.q_mn ? C::kQ : BN * 128u);
+      constexpr uint32_t bytes = C::kP + C::kQ;
       for (int kb = 0; kb < nkb; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort, p.fault_site + 1)) break;
         mbar_arrive_expect_tx(&full[stage], bytes);
@@ -688,7 +693,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2)
         } else {
           tma_load_2d(a_dst, &maps.p, &full[stage], kc, p0);
         }
-        if (p.q_mn) {
+        if constexpr (QMN) {
           for (uint32_t b = 0; b < C::kQ / LIN_BOX_MN; ++b)
             tma_load_2d(b_dst + b * LIN_BOX_MN, &maps.q, &full[stage], static_cast<int>(q0) + b * 64, kc);
         } else {
@@ -708,8 +713,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = lin_idesc(128, BN, p.bf16 != 0, p.p_mn != 0, p.q_mn != 0);
-      const uint32_t a_step = p.p_mn ? 2048u : 32u, b_step = p.q_mn ? 2048u : 32u;
+      const uint32_t idesc = lin_idesc(128, BN, p.bf16 != 0, p.p_mn != 0, QMN);
+      const uint32_t a_step = p.p_mn ? 2048u : 32u, b_step = QMN ? 2048u : 32u;
       int stage = 0;
       uint32_t phase = 0;
       for (int kb = 0; kb < nkb; ++kb) {
@@ -718,7 +723,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2)
         const uint32_t a_addr = smem_u32(smem + stage * C::kStage);
         const uint32_t b_addr = a_addr + C::kP;
         const uint64_t ad = p.p_mn ? sw128_mnmajor_desc(a_addr) : sw128_kmajor_desc(a_addr);
-        const uint64_t bd = p.q_mn ? sw128_mnmajor_desc(b_addr) : sw128_kmajor_desc(b_addr);
+        const uint64_t bd = QMN ? sw128_mnmajor_desc(b_addr) : sw128_kmajor_desc(b_addr);
 #pragma unroll
         for (int kk = 0; kk < LIN_BK / 16; ++kk)
           tc_mma_bf16(tmem_base, ad + ((kk * a_step) >> 4), bd + ((kk * b_step) >> 4), idesc, (kb | kk) != 0 ? 1u : 0u);
@@ -799,6 +804,8 @@ template <typename T>
 __global__ void __launch_bounds__(LIN_DP_THREADS)
     linear_dp_kernel(const T* __restrict__ dy, const T* __restrict__ pre, T* __restrict__ dp, float* __restrict__ part,
                      long long M, int N, long long rows, int act) {
+  pdl_next();
+  pdl_wait();
   const int col = (blockIdx.x * LIN_DP_THREADS + threadIdx.x) * 8;
   if (col >= N) return;
   const long long r0 = blockIdx.y * rows, r1 = min(M, r0 + rows);

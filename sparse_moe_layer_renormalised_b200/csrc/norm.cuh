@@ -281,6 +281,8 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS, 1) norm_kernel(const NormPar
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ int abort_flag;
   if (threadIdx.x == 0) abort_flag = 0;
+  pdl_next();
+  pdl_wait();
   NormRing<T, 1, NW, ALIGNED, PAR> r(p, norm_smem);
   __syncthreads();
   int s = 0, buf = 0;
@@ -363,6 +365,8 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ int abort_flag;
   if (threadIdx.x == 0) abort_flag = 0;
+  pdl_next();
+  pdl_wait();
   NormRing<T, 2, NW, ALIGNED, PAR> r(p, norm_smem);
   __syncthreads();
   F2 dg[NW][NP], db[NW][NP];
@@ -479,6 +483,8 @@ __global__ void __launch_bounds__(32 * COLSUM_SLICES)
     column_sum_kernel(const float* __restrict__ part, int parts, int width, int H, float* __restrict__ a_out,
                       float* __restrict__ b_out) {
   __shared__ float red[COLSUM_SLICES][32 * W];
+  pdl_next();
+  pdl_wait();
   const int c = (blockIdx.x * 32 + threadIdx.x) * W;
   float a[W];
 #pragma unroll

@@ -18,7 +18,28 @@ bool ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
 bool ws_fits(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws != nullptr && (reinterpret_cast<uintptr_t>(ws) % kAlign) == 0 && have >= need);
 }
-moe_status launched() { return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+// Launches a kernel so that it may be set up before the one ahead of it in the
+// stream has ended (its pdl_wait() waits for that); `cluster` CTAs a cluster.
+template <typename K, typename... A>
+cudaError_t op_launch(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  ++g_last_launches;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 // Calls f with a value of the element type of dtype t.
 template <typename F>
@@ -150,9 +171,7 @@ template <typename K>
 moe_status norm_launch(K kern, const NormParams& p, const NormPlan& q, cudaStream_t s) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(q.smem)) != cudaSuccess)
     return MOE_ERR_CUDA;
-  kern<<<q.blocks, q.tpg * q.groups, q.smem, s>>>(p);
-  ++g_last_launches;
-  return launched();
+  return op_launch(kern, q.blocks, q.tpg * q.groups, q.smem, s, 0, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 template <typename T, bool ALIGNED, bool PAR, bool BACKWARD>
@@ -201,13 +220,12 @@ moe_status norm_run(const moe_norm_desc& d, NormParams p, cudaStream_t s) {
 }
 
 // Column sums of part[parts][width] (see column_sum_kernel).
-void column_sums(const float* part, int parts, int width, int H, float* a_out, float* b_out, cudaStream_t s) {
+moe_status column_sums(const float* part, int parts, int width, int H, float* a_out, float* b_out, cudaStream_t s) {
   const dim3 block(32, COLSUM_SLICES);
-  if (width % 4 == 0)
-    column_sum_kernel<4><<<static_cast<unsigned>(cdiv(width, 128)), block, 0, s>>>(part, parts, width, H, a_out, b_out);
-  else
-    column_sum_kernel<1><<<static_cast<unsigned>(cdiv(width, 32)), block, 0, s>>>(part, parts, width, H, a_out, b_out);
-  ++g_last_launches;
+  const cudaError_t e =
+      width % 4 == 0 ? op_launch(column_sum_kernel<4>, static_cast<unsigned>(cdiv(width, 128)), block, 0, s, 0, part, parts, width, H, a_out, b_out)
+                     : op_launch(column_sum_kernel<1>, static_cast<unsigned>(cdiv(width, 32)), block, 0, s, 0, part, parts, width, H, a_out, b_out);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------------------ linear
@@ -295,7 +313,6 @@ cudaError_t lin_launch_wide(const LinProblem& g, LinParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(LW_THREADS);
   cfg.dynamicSmemBytes = LW_SMEM;
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -320,48 +337,40 @@ cudaError_t lin_launch_wide(const LinProblem& g, LinParams& p, cudaStream_t s) {
         (p.pre != nullptr && !lin_box_map(&maps.pre, p.pre, g.Q, g.P)))
       return cudaErrorInvalidValue;
   }
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(pairs, w.items())));
-  e = cudaLaunchKernelEx(&cfg, kern, maps, p);
-  ++g_last_launches;
+  e = op_launch(kern, 2 * static_cast<unsigned>(std::min<long long>(pairs, w.items())), LW_THREADS, LW_SMEM, s, 2, maps, p);
   const long long rest = static_cast<long long>(w.p_tiles) * w.q_tiles - w.full;
-  if (e == cudaSuccess && rest > 0) {
-    linear_fixup_kernel<OutT><<<static_cast<unsigned>(rest * (w.bn / 4)), 256, 0, s>>>(p);
-    ++g_last_launches;
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && rest > 0)
+    e = op_launch(linear_fixup_kernel<OutT>, static_cast<unsigned>(rest * (w.bn / 4)), 256, 0, s, 0, p);
   return e;
 }
 
-template <typename OutT, int BN>
-cudaError_t lin_launch_skinny(const LinProblem& g, LinParams& p, cudaStream_t s) {
-  auto kern = linear_skinny_kernel<OutT, BN>;
+template <typename OutT, int BN, bool QMN>
+cudaError_t lin_launch_skinny_inst(const LinProblem& g, LinParams& p, cudaStream_t s) {
+  using C = LsCfg<BN, QMN>;
+  auto kern = linear_skinny_kernel<OutT, BN, QMN>;
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(LsCfg<BN>::kSmem));
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
   p.bn = BN;
   p.p_tiles = static_cast<int>(cdiv(g.P, 128));
   p.q_tiles = static_cast<int>(cdiv(g.Q, BN));
-  // as many CTAs on the sum as two per SM allow, each with a few blocks of it
+  // as many CTAs on the sum as the SMs hold with certainty, two each (clusters have to
+  // fit their part of the chip: at 1.9 a SM some waited for others, 16.9 instead of
+  // 15.9 us at 4 x 7168 x 3584), each with a few blocks of it
   const long long tiles = static_cast<long long>(p.p_tiles) * p.q_tiles;
   const int split = static_cast<int>(
-      std::max<long long>(1, std::min<long long>({LS_MAX_SPLIT, 2LL * num_sms() / tiles, p.nkb / 2})));
+      std::max<long long>(1, std::min<long long>({LS_MAX_SPLIT, 16LL * num_sms() / 10 / tiles, p.nkb / 2})));
   LinMaps maps;
   std::memset(&maps, 0, sizeof maps);
   if (!lin_map(&maps.p, g.p, g.p_mn, g.P, g.R, 128) || !lin_map(&maps.q, g.q, g.q_mn, g.Q, g.R, BN))
     return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.p_tiles * split), static_cast<unsigned>(p.q_tiles));
-  cfg.blockDim = dim3(LS_THREADS);
-  cfg.dynamicSmemBytes = LsCfg<BN>::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+  return op_launch(kern, dim3(static_cast<unsigned>(p.p_tiles * split), static_cast<unsigned>(p.q_tiles)), LS_THREADS,
+                   C::kSmem, s, split, maps, p);
+}
+
+template <typename OutT, int BN>
+cudaError_t lin_launch_skinny(const LinProblem& g, LinParams& p, cudaStream_t s) {
+  return g.q_mn ? lin_launch_skinny_inst<OutT, BN, true>(g, p, s) : lin_launch_skinny_inst<OutT, BN, false>(g, p, s);
 }
 
 template <typename OutT>
@@ -378,7 +387,6 @@ moe_status lin_product(const LinProblem& g, LinParams p, cudaStream_t s) {
         : g.Q <= 32 ? lin_launch_skinny<OutT, 32>(g, p, s)
         : g.Q <= 64 ? lin_launch_skinny<OutT, 64>(g, p, s)
                     : lin_launch_skinny<OutT, 128>(g, p, s);
-    ++g_last_launches;
   } else {
     e = lin_launch_wide<OutT>(g, p, s);
   }
@@ -455,21 +463,17 @@ moe_status clip_run(const moe_grad_tensor* list, int32_t count, bool max_norm_ki
       }
       if (chunks > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED;
       l.chunks = static_cast<int>(chunks);
+      cudaError_t e;
       if (pass == 0) {
-        if (max_norm_kind)
-          clip_norm_kernel<MAXT, true><<<blocks, CLIP_THREADS, 0, s>>>(l, partial + li * blocks);
-        else
-          clip_norm_kernel<MAXT, false><<<blocks, CLIP_THREADS, 0, s>>>(l, partial + li * blocks);
+        e = op_launch(max_norm_kind ? clip_norm_kernel<MAXT, true> : clip_norm_kernel<MAXT, false>, blocks, CLIP_THREADS, 0, s,
+                      0, l, partial + li * blocks);
       } else {
         float* out = li == 0 ? norm_out : nullptr;
         const int grid = std::max(1, std::min(blocks, l.chunks));
-        if (max_norm_kind)
-          clip_scale_kernel<MAXT, true><<<grid, CLIP_THREADS, 0, s>>>(l, partial, nl * blocks, max_norm, out);
-        else
-          clip_scale_kernel<MAXT, false><<<grid, CLIP_THREADS, 0, s>>>(l, partial, nl * blocks, max_norm, out);
+        e = op_launch(max_norm_kind ? clip_scale_kernel<MAXT, true> : clip_scale_kernel<MAXT, false>, grid, CLIP_THREADS, 0, s,
+                      0, l, static_cast<const double*>(partial), nl * blocks, max_norm, out);
       }
-      ++g_last_launches;
-      if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+      if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
   }
   return MOE_OK;
@@ -494,15 +498,15 @@ moe_status moe_route(const moe_route_desc* d, const void* logits, const float* b
   p.w = w;
   const unsigned blocks = static_cast<unsigned>(cdiv(d->T, ROUTE_WARPS));
   const size_t smem = static_cast<size_t>(ROUTE_WARPS) * route_warp_bytes(d->E, d->keep_groups < d->groups);
+  cudaError_t e = cudaSuccess;
   with_type(d->dtype, [&](auto v) {
     using T = decltype(v);
     route_dispatch<T>(d->E, [&](auto vl, auto ch) {
-      route_kernel<T, decltype(vl)::value, decltype(ch)::value>
-          <<<blocks, ROUTE_WARPS * 32, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+      e = op_launch(route_kernel<T, decltype(vl)::value, decltype(ch)::value>, blocks, ROUTE_WARPS * 32, smem,
+                    reinterpret_cast<cudaStream_t>(stream), 0, p);
     });
   });
-  g_last_launches = 1;
-  return launched();
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_route_backward(const moe_route_desc* d, const void* logits, const int32_t* idx, const float* dw,
@@ -516,15 +520,15 @@ moe_status moe_route_backward(const moe_route_desc* d, const void* logits, const
   p.logits = logits;
   const unsigned blocks = static_cast<unsigned>(cdiv(d->T, ROUTE_WARPS));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
   with_type(d->dtype, [&](auto v) {
     using T = decltype(v);
     route_dispatch<T>(d->E, [&](auto vl, auto ch) {
-      route_backward_kernel<T, decltype(vl)::value, decltype(ch)::value>
-          <<<blocks, ROUTE_WARPS * 32, 0, s>>>(p, idx, dw, static_cast<T*>(dlogits));
+      e = op_launch(route_backward_kernel<T, decltype(vl)::value, decltype(ch)::value>, blocks, ROUTE_WARPS * 32, 0, s, 0,
+                    p, idx, dw, static_cast<T*>(dlogits));
     });
   });
-  g_last_launches = 1;
-  return launched();
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_norm(const moe_norm_desc* d, const void* x, const float* gamma, const float* beta, void* y, float* mean,
@@ -581,8 +585,8 @@ moe_status moe_norm_backward(const moe_norm_desc* d, const void* dy, const void*
     if (st != MOE_OK) return st;
   }
   if (dgamma != nullptr || dbeta != nullptr)
-    column_sums(part, d->T > 0 ? norm_plan(*d, true).blocks : 0, 2 * d->H, d->H, dgamma, dbeta, s);
-  return launched();
+    return column_sums(part, d->T > 0 ? norm_plan(*d, true).blocks : 0, 2 * d->H, d->H, dgamma, dbeta, s);
+  return MOE_OK;
 }
 
 size_t moe_linear_workspace_size(const moe_linear_desc* d) {
@@ -649,16 +653,11 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, const v
     const dim3 grid(static_cast<unsigned>(cdiv(d->N, LIN_DP_THREADS * 8)), static_cast<unsigned>(cdiv(d->M, rows)));
     auto run = [&](auto v) {
       using T = decltype(v);
-      linear_dp_kernel<T><<<grid, LIN_DP_THREADS, 0, s>>>(static_cast<const T*>(dy), static_cast<const T*>(pre),
-                                                          static_cast<T*>(to), part, d->M, d->N, rows, d->act);
+      return op_launch(linear_dp_kernel<T>, grid, LIN_DP_THREADS, 0, s, 0, static_cast<const T*>(dy), static_cast<const T*>(pre),
+                       static_cast<T*>(to), part, static_cast<long long>(d->M), d->N, rows, static_cast<int>(d->act));
     };
-    if (d->dtype == MOE_BF16)
-      run(__nv_bfloat16());
-    else
-      run(__half());
-    ++g_last_launches;
-    if (dbias != nullptr) column_sums(part, static_cast<int>(grid.y), d->N, d->N, dbias, nullptr, s);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if ((d->dtype == MOE_BF16 ? run(__nv_bfloat16()) : run(__half())) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dbias != nullptr && (st = column_sums(part, static_cast<int>(grid.y), d->N, d->N, dbias, nullptr, s)) != MOE_OK) return st;
     if (act) dp = to;
   }
   LinParams p{};

@@ -10,6 +10,14 @@
 
 namespace moe {
 
+// Programmatic dependent launch: a kernel launched with op_launch may be set up
+// while the one before it in the stream still runs, and touches no memory before
+// pdl_wait(), which returns when that one is complete and its writes are visible.
+// pdl_next() says that the kernel after may be set up from here on (once every
+// block has said so or has ended).  Without the launch attribute both do nothing.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Elements of a 16-byte load.
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));

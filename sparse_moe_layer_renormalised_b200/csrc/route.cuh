@@ -276,6 +276,8 @@ template <typename T, int VL, int CH>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32, 8) route_kernel(const RouteParams p) {
   constexpr int NV = VL * CH;
   extern __shared__ __align__(16) uint8_t route_smem[];
+  pdl_next();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const long long t = static_cast<long long>(blockIdx.x) * ROUTE_WARPS + warp;
@@ -571,6 +573,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 8)
     route_backward_kernel(const RouteParams p, const int32_t* __restrict__ idx, const float* __restrict__ dw,
                           T* __restrict__ dl_out) {
   constexpr int NV = VL * CH;
+  pdl_next();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const long long t = static_cast<long long>(blockIdx.x) * ROUTE_WARPS + (threadIdx.x >> 5);
   if (t >= p.T) return;
