@@ -11,9 +11,10 @@
 // Rows are read and written in 16-byte windows of the memory they lie in: where
 // the row length is no multiple of a window, row t starts `a` elements into one,
 // a = t H mod VL (VL elements a window), and window v holds the columns
-// v VL - a ... + VL - 1.  The rows of a group all have the same `a`.  The first and
-// the last window of such a row hold columns of its neighbours too, which are
-// masked on reading and left alone on writing.
+// v VL - a ... + VL - 1.  The rows of a block all have the same `a` (they lie a
+// multiple of VL rows apart).  The first and the last window of such a row hold
+// columns of its neighbours too, which are masked on reading and left alone on
+// writing.
 //
 // Forward: the variance is that of the centred values (no sum of squares minus
 // square of sums).  Backward: x and dy are read once; the sums of dgamma and dbeta
@@ -42,10 +43,10 @@ struct NormParams {
   int rms;
   int tpg;         // threads of a group, whole warps
   int groups;      // groups of a block
-  int walkers;     // groups of the grid that take rows: group i takes i, i + walkers, ...
   int stages;      // of a group's ring
   int row_bytes;   // of a row's windows in a stage
   int par_floats;  // of gamma (and as many of beta) in shared memory; 0: read where they lie
+  long long walkers;  // gridDim.x * groups: group g of block b takes rows g gridDim.x + b, + walkers, ...
 };
 
 constexpr int kFaultNormWait = 16;
@@ -76,11 +77,10 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
 __host__ __device__ constexpr size_t norm_head(int groups) {
   return static_cast<size_t>(groups) * (NORM_MAX_RING * 8 + 2 * 32 * 8);
 }
-// gamma and beta lie in shared memory with this much before and behind them, so
-// that the first and last windows need no bounds; where a window has two quads of
-// them, the even quads lie before the odd ones, so that a warp reads neighbours
-// (in their own order each read is a two-way bank conflict).
-constexpr int NORM_PAD = 8;
+// gamma and beta lie in shared memory by window, in the place of the block's rows;
+// where a window has two quads of them, the even quads lie before the odd ones, so
+// that a warp reads neighbours (in their own order each read is a two-way bank
+// conflict).
 
 // A group's place and its ring of OPS operands (x, or x and dy).
 template <typename T, int OPS, int NW, bool ALIGNED, bool PAR>
@@ -110,15 +110,13 @@ struct NormRing {
     op_b = p.row_bytes;
     stage_b = OPS * op_b;
     ring = reinterpret_cast<uint8_t*>(par0 + (OPS == 1 ? 2 : 1) * p.par_floats) + static_cast<size_t>(g) * p.stages * stage_b;
-    const int gid = blockIdx.x * p.groups + g;
-    first = gid < p.walkers ? gid : p.T;
-    a = ALIGNED || first >= p.T ? 0 : static_cast<int>(first * p.H % VL);
+    first = static_cast<long long>(g) * gridDim.x + blockIdx.x;
+    a = ALIGNED ? 0 : static_cast<int>(static_cast<long long>(blockIdx.x) * p.H % VL);
     v0 = warp * 32 * NW + lane;
     col0 = v0 * VL - a;
     mine = smem_u32(ring) + v0 * 16;
-    const int q0 = (NORM_PAD + col0) >> 2;  // the quad that the first column is in
-    par[0] = smem_u32(par0 + quad(q0));
-    par[1] = smem_u32(par0 + quad(q0 + 1));
+    par[0] = smem_u32(par0 + quad(v0 * (VL / 4)));
+    par[1] = smem_u32(par0 + quad(v0 * (VL / 4) + 1));
     if (tid == 0) {
       for (int i = 0; i < p.stages; ++i) mbar_init(&bars[i], 1);
       fence_mbar_init();
@@ -132,10 +130,10 @@ struct NormRing {
         const float none = k == 0 ? 1.f : 0.f;
 #pragma unroll 4
         for (int i = threadIdx.x; i < p.par_floats / 4; i += blockDim.x) {
-          const int j = 4 * i - NORM_PAD;
+          const int j = 4 * i - a;
           float4 v = make_float4(none, none, none, none);
           if (from[k] != nullptr) {
-            if (j >= 0 && j + 4 <= p.H) {
+            if ((a & 3) == 0 && j >= 0 && j + 4 <= p.H) {
               v = *reinterpret_cast<const float4*>(from[k] + j);
             } else {
               if (inside(j)) v.x = from[k][j];
@@ -243,34 +241,24 @@ struct NormRing {
     }
   }
   // gamma (k = 0) or beta (1) of window w: from shared memory, or (PAR false) from
-  // `q` or, without one, `none`.  Columns that start inside a quad come as the quads
-  // around them, shifted.
+  // `q` or, without one, `none`.
   __device__ __forceinline__ void param(int k, const float* q, float none, int w, F2* f) const {
+    float v[VL];
     if constexpr (!PAR) {
-      float v[VL];
       if (q == nullptr) {
 #pragma unroll
         for (int i = 0; i < VL; ++i) v[i] = none;
       } else {
         op_load_f32<VL>(q + col(w), v);
       }
-#pragma unroll
-      for (int i = 0; i < VL; i += 2) f[i / 2] = f2(v[i], v[i + 1]);
     } else {
       // 32 windows on are 32 quads on in either half, or 32 in all (VL = 4)
       const uint32_t at = static_cast<uint32_t>(k * p.par_floats * 4 + w * 512);
-      float v[VL + 4];
       op_unpack16<float>(ld_shared16(par[0] + at), v);
       if constexpr (VL == 8) op_unpack16<float>(ld_shared16(par[1] + at), v + 4);
-      const int o = ALIGNED ? 0 : (NORM_PAD - a) & 3;
-      if (o != 0) {
-        op_unpack16<float>(ld_shared16((VL == 8 ? par[0] + 16 : par[1]) + at), v + VL);
-#pragma unroll
-        for (int i = 0; i < VL; ++i) v[i] = o == 1 ? v[i + 1] : o == 2 ? v[i + 2] : v[i + 3];
-      }
-#pragma unroll
-      for (int i = 0; i < VL; i += 2) f[i / 2] = f2(v[i], v[i + 1]);
     }
+#pragma unroll
+    for (int i = 0; i < VL; i += 2) f[i / 2] = f2(v[i], v[i + 1]);
   }
 };
 
@@ -449,28 +437,39 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
     }
   }
 
-  // the groups' sums in group order, by column, in the memory of the rows (every
-  // copy has been waited for)
-  __syncthreads();
-  float* acc = reinterpret_cast<float*>(norm_smem + norm_head(p.groups)) + p.par_floats;
-  for (int g = 0; g < p.groups; ++g) {
-    if (r.g == g) {
-#pragma unroll
-      for (int w = 0; w < NW; ++w)
-#pragma unroll
-        for (int i = 0; i < VL; ++i) {
-          const int j = r.col(w) + i;
-          if (!r.inside(j)) continue;
-          const float2 e = f2_get(dg[w][i / 2]), d = f2_get(db[w][i / 2]);
-          const float de = i & 1 ? e.y : e.x, dd = i & 1 ? d.y : d.x;
-          acc[j] = g == 0 ? de : acc[j] + de;
-          acc[p.H + j] = g == 0 ? dd : acc[p.H + j] + dd;
-        }
-    }
-    __syncthreads();
-  }
+  // the groups' sums side by side in the memory of the rows (every copy has been
+  // waited for), then added in group order
   float* part = p.part + static_cast<long long>(blockIdx.x) * 2 * p.H;
-  for (int c = threadIdx.x; c < 2 * p.H; c += blockDim.x) part[c] = acc[c];
+  float* acc = part;
+  if (p.groups > 1) {
+    __syncthreads();
+    acc = reinterpret_cast<float*>(norm_smem + norm_head(p.groups)) + p.par_floats + static_cast<size_t>(r.g) * 2 * p.H;
+  }
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+#pragma unroll
+    for (int i = 0; i < VL; i += 2) {
+      const int j = r.col(w) + i;
+      const float2 e = f2_get(dg[w][i / 2]), d = f2_get(db[w][i / 2]);
+      if (ALIGNED) {
+        if (j < p.H) {
+          *reinterpret_cast<float2*>(acc + j) = e;
+          *reinterpret_cast<float2*>(acc + p.H + j) = d;
+        }
+      } else {
+        if (r.inside(j)) acc[j] = e.x, acc[p.H + j] = d.x;
+        if (r.inside(j + 1)) acc[j + 1] = e.y, acc[p.H + j + 1] = d.y;
+      }
+    }
+  if (p.groups > 1) {
+    __syncthreads();
+    const float* all = reinterpret_cast<const float*>(norm_smem + norm_head(p.groups)) + p.par_floats;
+    for (int c = threadIdx.x; c < 2 * p.H; c += blockDim.x) {
+      float v = 0.f;
+      for (int g = 0; g < p.groups; ++g) v += all[static_cast<size_t>(g) * 2 * p.H + c];
+      part[c] = v;
+    }
+  }
 }
 
 // Sum of column c of part[parts][width], in order within each of 16 slices, then
@@ -490,12 +489,20 @@ __global__ void __launch_bounds__(32 * COLSUM_SLICES)
 #pragma unroll
   for (int i = 0; i < W; ++i) a[i] = 0.f;
   if (c < width) {
-#pragma unroll 10
-    for (int k = threadIdx.y; k < parts; k += COLSUM_SLICES) {
-      float v[W];
-      op_load_f32<W>(part + static_cast<long long>(k) * width + c, v);
+    constexpr int kBatch = 10;  // loads in flight
+    for (int k0 = threadIdx.y; k0 < parts; k0 += kBatch * COLSUM_SLICES) {
+      float v[kBatch][W];
 #pragma unroll
-      for (int i = 0; i < W; ++i) a[i] += v[i];
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * COLSUM_SLICES;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[u][i] = 0.f;
+        if (k < parts) op_load_f32<W>(part + static_cast<long long>(k) * width + c, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int i = 0; i < W; ++i) a[i] += v[u][i];
     }
   }
 #pragma unroll

@@ -135,7 +135,7 @@ int norm_windows(const moe_norm_desc& d) {
 // as many groups as the block, the named barriers or the rows allow, and rings as
 // deep as the shared memory is.
 struct NormPlan {
-  int nw, tpg, groups, stages, row_bytes, par_floats, blocks, walkers;
+  int nw, tpg, groups, stages, row_bytes, par_floats, blocks;
   size_t smem;
 };
 NormPlan norm_plan(const moe_norm_desc& d, bool backward) {
@@ -149,21 +149,23 @@ NormPlan norm_plan(const moe_norm_desc& d, bool backward) {
   q.groups = static_cast<int>(std::max<long long>(1, std::min<long long>(q.groups, cdiv(d.T, num_sms()))));
   q.row_bytes = windows * 16;
   // gamma and beta in shared memory, unless rows of whole windows are so long that
-  // they would take the ring's place, or so few that no group takes a second one
-  if (!norm_aligned(d) || (d.H <= 8192 && d.T > static_cast<long long>(q.groups) * num_sms()))
-    q.par_floats = static_cast<int>(round_up(d.H + 2 * NORM_PAD, 8));
+  // they would leave less than two stages, or so few that no group takes a second one
+  const size_t par_bytes = static_cast<size_t>(windows) * vl * (backward ? 4 : 8);
+  if (!norm_aligned(d) || (par_bytes + 2 * static_cast<size_t>(ops) * q.row_bytes <= 224 * 1024 &&
+                           d.T > static_cast<long long>(q.groups) * num_sms()))
+    q.par_floats = windows * vl;
   // three stages at least are worth a group
   for (;; --q.groups) {
     const size_t head = norm_head(q.groups) + static_cast<size_t>(q.par_floats) * (backward ? 4 : 8);
     const size_t group = static_cast<size_t>(ops) * q.row_bytes * q.groups;
     q.stages = static_cast<int>(std::max<size_t>(1, std::min<size_t>(NORM_MAX_RING, (226 * 1024 - head) / group)));
-    q.smem = head + std::max<size_t>(group * q.stages, backward ? static_cast<size_t>(d.H) * 8 : 0);
+    q.smem = head + std::max<size_t>(group * q.stages, backward && q.groups > 1 ? static_cast<size_t>(q.groups) * d.H * 8 : 0);
     if (q.stages >= 3 || q.groups <= 2) break;
   }
   q.blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(cdiv(d.T, q.groups), num_sms())));
-  // rows of one group start at one offset in a window: a stride of whole windows
-  q.walkers = q.blocks * q.groups;
-  if (!norm_aligned(d) && q.walkers < d.T) q.walkers -= q.walkers % vl;
+  // the rows of a block start at one offset in a window: they lie as many rows apart
+  // as there are blocks, a multiple of a window's elements (or are one a block)
+  if (!norm_aligned(d) && d.T > q.blocks) q.blocks = std::max(vl, q.blocks - q.blocks % vl);
   return q;
 }
 
@@ -205,7 +207,7 @@ moe_status norm_run(const moe_norm_desc& d, NormParams p, cudaStream_t s) {
   p.rms = d.kind == MOE_NORM_RMS;
   p.tpg = q.tpg;
   p.groups = q.groups;
-  p.walkers = q.walkers;
+  p.walkers = static_cast<long long>(q.blocks) * q.groups;
   p.stages = q.stages;
   p.row_bytes = q.row_bytes;
   p.par_floats = q.par_floats;
