@@ -2,7 +2,11 @@
 // (or takes the largest magnitude) into one fp64 partial per block, and one that
 // reads the partials, forms the factor and scales.  Both are bound by memory;
 // the second walks the chunks backwards, so that what the first read last is
-// still in L2.
+// still in L2.  In the first a block takes a run of chunks that follow one another
+// and so looks at few entries of the list, which is slow to index; in the second
+// chunks are dealt out in turn, which the writes prefer (for 322M fp32 gradients
+// 205 against 238 us in the first pass, 445 against 490 in the second).  Chunks
+// inside a tensor, nearly all, go without bounds.
 //
 // The tensor list travels in the kernel's parameters (at most CLIP_MAX tensors
 // a launch), so a captured graph holds it and nothing has to be copied.
@@ -12,7 +16,8 @@
 
 namespace moe {
 
-constexpr int CLIP_THREADS = 512;
+constexpr int CLIP_THREADS = 256;
+constexpr int CLIP_LOADS = 8;  // in flight a thread
 constexpr int CLIP_MAX = 1024;  // 29 bytes of parameters each, below the 32764 a launch may have
 
 enum ClipType : uint8_t { kClipF32 = 0, kClipBF16 = 1, kClipF16 = 2 };
@@ -25,7 +30,7 @@ struct ClipList {
   int first[MAXT];  // number of chunks before the tensor's
   uint8_t type[MAXT];
   int count, chunks;
-  int chunk;  // elements of a chunk: a multiple of 64, so chunks keep a tensor's alignment
+  int chunk;  // 16-byte vectors of a chunk; chunks start at whole vectors of the input's memory
 };
 
 // The tensor of chunk c: the last one whose first chunk is not after c.
@@ -42,6 +47,34 @@ __device__ __forceinline__ int clip_find(const ClipList<MAXT>& l, int c) {
   return lo;
 }
 
+// The tensor of the chunk at hand.
+template <int MAXT>
+struct ClipCursor {
+  const ClipList<MAXT>& l;
+  int k = -1, lo = 0, hi = 0;  // tensor, its chunks [lo, hi)
+  const void* in = nullptr;
+  void* out = nullptr;
+  long long n = 0;
+  int type = 0;
+  __device__ __forceinline__ explicit ClipCursor(const ClipList<MAXT>& list) : l(list) {}
+  __device__ __forceinline__ void seek(int c) {
+    if (c >= lo && c < hi) return;
+    k = c == hi && k >= 0 ? k + 1 : clip_find(l, c);
+    lo = l.first[k];
+    hi = k + 1 < l.count ? l.first[k + 1] : l.chunks;
+    in = l.in[k];
+    out = l.out[k];
+    n = l.n[k];
+    type = l.type[k];
+  }
+};
+
+// The chunks of block b of nb: [first, second).
+__device__ __forceinline__ int2 clip_share(int chunks, int b, int nb) {
+  return make_int2(static_cast<int>(static_cast<long long>(chunks) * b / nb),
+                   static_cast<int>(static_cast<long long>(chunks) * (b + 1) / nb));
+}
+
 // Squares of one 16-byte vector (or one element): added up in fp32, and again in
 // fp64 where the fp32 sum may have overflowed, lost small squares or met a NaN.
 template <typename T, int VL>
@@ -56,12 +89,10 @@ __device__ __forceinline__ double clip_squares(const float* f) {
   return d;
 }
 
-// Elements before the first 16-byte boundary of p (at most n).
+// Elements before p in its 16-byte vector.
 template <typename T>
-__device__ __forceinline__ int clip_head(const T* p, int n) {
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
-  const int h = off ? (16 - off) / static_cast<int>(sizeof(T)) : 0;
-  return h < n ? h : n;
+__device__ __forceinline__ int clip_skew(const T* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) / static_cast<int>(sizeof(T));
 }
 
 template <int V>
@@ -69,11 +100,53 @@ struct ClipWidth {
   static constexpr int value = V;
 };
 
-template <typename T, bool MAX>
-__device__ __forceinline__ void clip_reduce_chunk(const T* p, int n, double& sum, uint32_t& top) {
+// Calls take(elements, how many, index) for the elements of vectors [v0, v0 + nv) of
+// a tensor of n elements at p, counted from the vector that p lies in; nv is a
+// multiple of CLIP_LOADS * CLIP_THREADS.
+template <typename T, typename F>
+__device__ __forceinline__ void clip_chunk(const T* p, long long n, long long v0, int nv, F take) {
   constexpr int VL = kVec<T>;
-  const int head = clip_head(p, n);
-  auto take = [&](const float* f, auto vl) {
+  const int skew = clip_skew(p);
+  const T* base = p - skew;  // (only dereferenced inside the tensor)
+  const long long end = n + skew;
+  if (v0 * VL >= skew && (v0 + nv) * VL <= end) {
+    const uint4* q = reinterpret_cast<const uint4*>(base) + v0;
+    const long long e0 = v0 * VL - skew;
+    for (int i = threadIdx.x; i < nv; i += CLIP_LOADS * CLIP_THREADS) {
+      uint4 a[CLIP_LOADS];
+#pragma unroll
+      for (int u = 0; u < CLIP_LOADS; ++u) a[u] = q[i + u * CLIP_THREADS];
+#pragma unroll
+      for (int u = 0; u < CLIP_LOADS; ++u) {
+        float f[VL];
+        op_unpack16<T>(a[u], f);
+        take(f, ClipWidth<VL>(), e0 + (i + u * CLIP_THREADS) * VL);
+      }
+    }
+    return;
+  }
+  // a chunk at an end of the tensor: element by element where a vector is cut
+  const long long last = min(v0 + nv, (end + VL - 1) / VL);
+  for (long long v = v0 + threadIdx.x; v < last; v += CLIP_THREADS) {
+    const long long e = v * VL;
+    if (e >= skew && e + VL <= end) {
+      float f[VL];
+      op_unpack16<T>(reinterpret_cast<const uint4*>(base)[v], f);
+      take(f, ClipWidth<VL>(), e - skew);
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < VL; ++j) {
+        if (e + j < skew || e + j >= end) continue;
+        const float f = op_f32(base[e + j]);
+        take(&f, ClipWidth<1>(), e + j - skew);
+      }
+    }
+  }
+}
+
+template <typename T, bool MAX>
+__device__ __forceinline__ void clip_reduce_chunk(const void* p, long long n, long long v0, int nv, double& sum, uint32_t& top) {
+  clip_chunk(static_cast<const T*>(p), n, v0, nv, [&](const float* f, auto vl, long long) {
     constexpr int W = decltype(vl)::value;
     if constexpr (MAX) {
       // magnitudes as integers: a NaN is above everything and stays
@@ -82,35 +155,7 @@ __device__ __forceinline__ void clip_reduce_chunk(const T* p, int n, double& sum
     } else {
       sum += clip_squares<T, W>(f);
     }
-  };
-  if (static_cast<int>(threadIdx.x) < head) {
-    const float f = op_f32(p[threadIdx.x]);
-    take(&f, ClipWidth<1>());
-  }
-  const uint4* q = reinterpret_cast<const uint4*>(p + head);
-  const int nv = (n - head) / VL;
-  int i = threadIdx.x;
-  for (; i + 3 * CLIP_THREADS < nv; i += 4 * CLIP_THREADS) {
-    uint4 a[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) a[u] = q[i + u * CLIP_THREADS];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float f[VL];
-      op_unpack16<T>(a[u], f);
-      take(f, ClipWidth<VL>());
-    }
-  }
-  for (; i < nv; i += CLIP_THREADS) {
-    float f[VL];
-    op_unpack16<T>(q[i], f);
-    take(f, ClipWidth<VL>());
-  }
-  const int done = head + nv * VL;
-  if (static_cast<int>(threadIdx.x) < n - done) {
-    const float f = op_f32(p[done + threadIdx.x]);
-    take(&f, ClipWidth<1>());
-  }
+  });
 }
 
 // partial[blockIdx.x] = the block's sum of squares, or largest magnitude.
@@ -122,16 +167,17 @@ __global__ void __launch_bounds__(CLIP_THREADS)
   pdl_wait();
   double sum = 0.0;
   uint32_t top = 0u;
-  for (int c = blockIdx.x; c < l.chunks; c += gridDim.x) {
-    const int k = clip_find(l, c);
-    const long long at = static_cast<long long>(c - l.first[k]) * l.chunk;
-    const int n = static_cast<int>(min(static_cast<long long>(l.chunk), l.n[k] - at));
-    if (l.type[k] == kClipF32)
-      clip_reduce_chunk<float, MAX>(static_cast<const float*>(l.in[k]) + at, n, sum, top);
-    else if (l.type[k] == kClipBF16)
-      clip_reduce_chunk<__nv_bfloat16, MAX>(static_cast<const __nv_bfloat16*>(l.in[k]) + at, n, sum, top);
+  ClipCursor<MAXT> cur(l);
+  const int2 share = clip_share(l.chunks, blockIdx.x, gridDim.x);
+  for (int c = share.x; c < share.y; ++c) {
+    cur.seek(c);
+    const long long v0 = static_cast<long long>(c - cur.lo) * l.chunk;
+    if (cur.type == kClipF32)
+      clip_reduce_chunk<float, MAX>(cur.in, cur.n, v0, l.chunk, sum, top);
+    else if (cur.type == kClipBF16)
+      clip_reduce_chunk<__nv_bfloat16, MAX>(cur.in, cur.n, v0, l.chunk, sum, top);
     else
-      clip_reduce_chunk<__half, MAX>(static_cast<const __half*>(l.in[k]) + at, n, sum, top);
+      clip_reduce_chunk<__half, MAX>(cur.in, cur.n, v0, l.chunk, sum, top);
   }
   if constexpr (MAX) sum = static_cast<double>(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
   else sum = warp_sum(sum);
@@ -148,42 +194,22 @@ __global__ void __launch_bounds__(CLIP_THREADS)
 }
 
 template <typename T>
-__device__ __forceinline__ void clip_scale_chunk(const T* p, T* o, int n, float coef) {
-  constexpr int VL = kVec<T>;
-  // one alignment for both: head, vectors, tail; else element by element
-  if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15u) != 0u) {
-    for (int i = threadIdx.x; i < n; i += CLIP_THREADS) o[i] = op_from<T>(op_f32(p[i]) * coef);
-    return;
-  }
-  const int head = clip_head(p, n);
-  if (static_cast<int>(threadIdx.x) < head) o[threadIdx.x] = op_from<T>(op_f32(p[threadIdx.x]) * coef);
-  const uint4* q = reinterpret_cast<const uint4*>(p + head);
-  uint4* r = reinterpret_cast<uint4*>(o + head);
-  const int nv = (n - head) / VL;
-  int i = threadIdx.x;
-  for (; i + 3 * CLIP_THREADS < nv; i += 4 * CLIP_THREADS) {
-    uint4 a[4];
+__device__ __forceinline__ void clip_scale_chunk(const void* p, void* out, long long n, long long v0, int nv, float coef) {
+  T* o = static_cast<T*>(out);
+  // one alignment for both: whole vectors are written as such
+  const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0u;
+  clip_chunk(static_cast<const T*>(p), n, v0, nv, [&](const float* f, auto vl, long long at) {
+    constexpr int W = decltype(vl)::value;
+    float g[W];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) a[u] = q[i + u * CLIP_THREADS];
+    for (int j = 0; j < W; ++j) g[j] = f[j] * coef;
+    if (W > 1 && same) {
+      if constexpr (W > 1) *reinterpret_cast<uint4*>(o + at) = op_pack16<T>(g);
+    } else {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float f[VL];
-      op_unpack16<T>(a[u], f);
-#pragma unroll
-      for (int j = 0; j < VL; ++j) f[j] *= coef;
-      r[i + u * CLIP_THREADS] = op_pack16<T>(f);
+      for (int j = 0; j < W; ++j) o[at + j] = op_from<T>(g[j]);
     }
-  }
-  for (; i < nv; i += CLIP_THREADS) {
-    float f[VL];
-    op_unpack16<T>(q[i], f);
-#pragma unroll
-    for (int j = 0; j < VL; ++j) f[j] *= coef;
-    r[i] = op_pack16<T>(f);
-  }
-  const int done = head + nv * VL;
-  if (static_cast<int>(threadIdx.x) < n - done)
-    o[done + threadIdx.x] = op_from<T>(op_f32(p[done + threadIdx.x]) * coef);
+  });
 }
 
 template <int MAXT, bool MAX>
@@ -223,19 +249,17 @@ __global__ void __launch_bounds__(CLIP_THREADS)
   }
   __syncthreads();
   const float coef = s_coef;
-  for (int b = blockIdx.x; b < l.chunks; b += gridDim.x) {
-    const int c = l.chunks - 1 - b;
-    const int k = clip_find(l, c);
-    if (coef == 1.0f && l.in[k] == l.out[k]) continue;
-    const long long at = static_cast<long long>(c - l.first[k]) * l.chunk;
-    const int n = static_cast<int>(min(static_cast<long long>(l.chunk), l.n[k] - at));
-    if (l.type[k] == kClipF32)
-      clip_scale_chunk(static_cast<const float*>(l.in[k]) + at, static_cast<float*>(l.out[k]) + at, n, coef);
-    else if (l.type[k] == kClipBF16)
-      clip_scale_chunk(static_cast<const __nv_bfloat16*>(l.in[k]) + at, static_cast<__nv_bfloat16*>(l.out[k]) + at, n,
-                       coef);
+  ClipCursor<MAXT> cur(l);
+  for (int c = l.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+    cur.seek(c);
+    if (coef == 1.0f && cur.in == cur.out) continue;
+    const long long v0 = static_cast<long long>(c - cur.lo) * l.chunk;
+    if (cur.type == kClipF32)
+      clip_scale_chunk<float>(cur.in, cur.out, cur.n, v0, l.chunk, coef);
+    else if (cur.type == kClipBF16)
+      clip_scale_chunk<__nv_bfloat16>(cur.in, cur.out, cur.n, v0, l.chunk, coef);
     else
-      clip_scale_chunk(static_cast<const __half*>(l.in[k]) + at, static_cast<__half*>(l.out[k]) + at, n, coef);
+      clip_scale_chunk<__half>(cur.in, cur.out, cur.n, v0, l.chunk, coef);
   }
 }
 

@@ -428,24 +428,29 @@ bool clip_list_ok(const moe_grad_tensor* list, int32_t count) {
 
 // Launches over the list and blocks of each.
 int clip_launches(int32_t count) { return std::max(1, static_cast<int>(cdiv(count, CLIP_MAX))); }
-int clip_blocks() { return 4 * num_sms(); }
+int clip_blocks() { return 8 * num_sms(); }
 
-// Elements of a chunk: about eight chunks a block over the whole list, so that
-// the blocks' shares are even, and at least 4096, so that a chunk's start-up is
-// small beside it.
-int clip_chunk(const moe_grad_tensor* list, int32_t count) {
+// 16-byte vectors that a tensor touches.
+long long clip_vectors(const moe_grad_tensor& t) {
+  const long long es = op_type_bytes(t.dtype), skew = static_cast<long long>(reinterpret_cast<uintptr_t>(t.in) & 15u) / es;
+  return cdiv((t.n + skew) * es, 16);
+}
+
+// Vectors of a chunk: 64 KB, or one round of a block's loads (32 KB) where the whole
+// list would not give every block a few.
+int clip_chunk_vectors(const moe_grad_tensor* list, int32_t count) {
   long long total = 0;
-  for (int i = 0; i < count; ++i) total += list[i].n;
-  long long c = total / (8LL * clip_blocks());
-  c = std::max<long long>(4096, std::min<long long>(c, 65536));
-  return static_cast<int>(c / 64 * 64);
+  for (int i = 0; i < count; ++i)
+    if (list[i].n > 0) total += clip_vectors(list[i]);
+  constexpr int kRound = CLIP_LOADS * CLIP_THREADS;
+  return total >= 8LL * kRound * clip_blocks() ? 2 * kRound : kRound;
 }
 
 template <int MAXT>
 moe_status clip_run(const moe_grad_tensor* list, int32_t count, bool max_norm_kind, float max_norm, float* norm_out,
                     double* partial, cudaStream_t s) {
   const int nl = clip_launches(count), blocks = clip_blocks();
-  const int chunk = clip_chunk(list, count);
+  const int chunk = clip_chunk_vectors(list, count);
   for (int pass = 0; pass < 2; ++pass) {
     for (int li = 0; li < nl; ++li) {
       ClipList<MAXT> l;
@@ -461,7 +466,7 @@ moe_status clip_run(const moe_grad_tensor* list, int32_t count, bool max_norm_ki
         l.n[k] = t.n;
         l.first[k] = static_cast<int>(chunks);
         l.type[k] = t.dtype == MOE_F32 ? kClipF32 : t.dtype == MOE_BF16 ? kClipBF16 : kClipF16;
-        chunks += cdiv(t.n, chunk);
+        chunks += cdiv(clip_vectors(t), chunk);
       }
       if (chunks > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED;
       l.chunks = static_cast<int>(chunks);
