@@ -123,7 +123,7 @@ def act(a, kind):
     if kind == "relu":
         return torch.where(a > 0, a, torch.zeros_like(a))
     if kind == "silu":
-        return a / (1.0 + torch.exp(-a))
+        return a * torch.sigmoid(a)  # (a / (1 + e^-a) has no gradient where e^-a overflows)
     if kind == "gelu":
         return 0.5 * a * (1.0 + torch.erf(a / math.sqrt(2.0)))
     if kind == "gelu_tanh":

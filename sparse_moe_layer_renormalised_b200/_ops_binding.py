@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _binding as _b
-from ._binding import _nbytes, _ptr, _stream
+from ._binding import _nbytes, _stream
 
 MOE_F16 = 5
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
@@ -90,6 +90,13 @@ def _lib() -> ctypes.CDLL:
             getattr(L, f).restype = sz if f.endswith("_size") else ctypes.c_int
         _ready = L
     return L
+
+
+def _ptr(t):
+    try:
+        return t.data_ptr()
+    except AttributeError:  # an address, or None
+        return t
 
 
 def route_desc(T: int, E: int, k: int, groups: int = 1, keep_groups: int | None = None, group_top: int = 1,

@@ -101,45 +101,53 @@ struct ClipWidth {
 };
 
 // Calls take(elements, how many, index) for the elements of vectors [v0, v0 + nv) of
-// a tensor of n elements at p, counted from the vector that p lies in; nv is a
-// multiple of CLIP_LOADS * CLIP_THREADS.
+// a tensor of n elements at p, counted from the vector that p lies in.
 template <typename T, typename F>
 __device__ __forceinline__ void clip_chunk(const T* p, long long n, long long v0, int nv, F take) {
   constexpr int VL = kVec<T>;
   const int skew = clip_skew(p);
   const T* base = p - skew;  // (only dereferenced inside the tensor)
   const long long end = n + skew;
-  if (v0 * VL >= skew && (v0 + nv) * VL <= end) {
-    const uint4* q = reinterpret_cast<const uint4*>(base) + v0;
-    const long long e0 = v0 * VL - skew;
-    for (int i = threadIdx.x; i < nv; i += CLIP_LOADS * CLIP_THREADS) {
-      uint4 a[CLIP_LOADS];
+  // the chunk's whole vectors
+  const long long lo = v0 == 0 && skew > 0 ? 1 : v0;
+  const int count = static_cast<int>(min(v0 + nv, end / VL) - lo);
+  const uint4* q = reinterpret_cast<const uint4*>(base) + lo;
+  const long long e0 = lo * VL - skew;
+  int i = threadIdx.x;
+  for (; i + (CLIP_LOADS - 1) * CLIP_THREADS < count; i += CLIP_LOADS * CLIP_THREADS) {
+    uint4 a[CLIP_LOADS];
 #pragma unroll
-      for (int u = 0; u < CLIP_LOADS; ++u) a[u] = q[i + u * CLIP_THREADS];
+    for (int u = 0; u < CLIP_LOADS; ++u) a[u] = q[i + u * CLIP_THREADS];
 #pragma unroll
-      for (int u = 0; u < CLIP_LOADS; ++u) {
-        float f[VL];
-        op_unpack16<T>(a[u], f);
-        take(f, ClipWidth<VL>(), e0 + (i + u * CLIP_THREADS) * VL);
-      }
-    }
-    return;
-  }
-  // a chunk at an end of the tensor: element by element where a vector is cut
-  const long long last = min(v0 + nv, (end + VL - 1) / VL);
-  for (long long v = v0 + threadIdx.x; v < last; v += CLIP_THREADS) {
-    const long long e = v * VL;
-    if (e >= skew && e + VL <= end) {
+    for (int u = 0; u < CLIP_LOADS; ++u) {
       float f[VL];
-      op_unpack16<T>(reinterpret_cast<const uint4*>(base)[v], f);
-      take(f, ClipWidth<VL>(), e - skew);
-    } else {
-#pragma unroll 1
-      for (int j = 0; j < VL; ++j) {
-        if (e + j < skew || e + j >= end) continue;
-        const float f = op_f32(base[e + j]);
-        take(&f, ClipWidth<1>(), e + j - skew);
-      }
+      op_unpack16<T>(a[u], f);
+      take(f, ClipWidth<VL>(), e0 + (i + u * CLIP_THREADS) * VL);
+    }
+  }
+  if (i < count) {
+    // the last round: all loads at once here too, what lies behind the end is not used
+    uint4 a[CLIP_LOADS];
+#pragma unroll
+    for (int u = 0; u < CLIP_LOADS; ++u) a[u] = q[min(i + u * CLIP_THREADS, count - 1)];
+#pragma unroll
+    for (int u = 0; u < CLIP_LOADS; ++u) {
+      if (i + u * CLIP_THREADS >= count) break;
+      float f[VL];
+      op_unpack16<T>(a[u], f);
+      take(f, ClipWidth<VL>(), e0 + (i + u * CLIP_THREADS) * VL);
+    }
+  }
+  // the elements of cut vectors: the tensor's first, in its first chunk, and its last,
+  // in the chunk they lie in (a tensor inside one vector: in the first alone)
+  if (threadIdx.x < 2 * VL) {
+    const int j = threadIdx.x & (VL - 1);
+    const long long v = threadIdx.x < VL ? 0 : end / VL;
+    const long long e = v * VL + j;
+    const bool cut = threadIdx.x < VL ? skew > 0 : end % VL != 0 && (v > 0 || skew == 0);
+    if (cut && v >= v0 && v < v0 + nv && e >= skew && e < end) {
+      const float f = op_f32(base[e]);
+      take(&f, ClipWidth<1>(), e - skew);
     }
   }
 }

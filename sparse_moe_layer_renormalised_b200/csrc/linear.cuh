@@ -62,7 +62,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // sigmoid by the fast exponential and reciprocal: relative error below 2^-23 (4 + 1.2 |a|).
-__device__ __forceinline__ float lin_sigmoid(float a) { return rcp_approx(1.0f + __expf(fminf(-a, 80.f))); }
+__device__ __forceinline__ float lin_sigmoid(float a) { return rcp_approx(1.0f + __expf(-a)); }
 
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
 
@@ -88,7 +88,8 @@ __device__ __forceinline__ float lin_act(float a, int act) {
       // a Phi(a) = max(a, 0) - |a| erfc(|a| / sqrt 2) / 2 on both sides of 0
       float e;
       const float c = lin_erfc_abs(a, &e);
-      return a == a ? fmaf(-0.5f * fabsf(a), c, fmaxf(a, 0.f)) : a;
+      // (beyond 100 c is 0: no product of an infinity with it)
+      return a == a ? fmaf(-0.5f * fminf(fabsf(a), 100.f), c, fmaxf(a, 0.f)) : a;
     }
     case kActGeluTanh:  // (1 + tanh u) / 2 = sigmoid(2 u)
       return a * lin_sigmoid(2.f * kSqrt2OverPi * (a + 0.044715f * a * a * a));
@@ -98,6 +99,8 @@ __device__ __forceinline__ float lin_act(float a, int act) {
 }
 
 __device__ __forceinline__ float lin_act_grad(float a, int act) {
+  // beyond 100 every slope is 0 or 1 to the last bit; no infinity meets a 0 there
+  if (fabsf(a) > 100.f) return act == kActNone ? 1.f : a > 0.f ? 1.f : 0.f;
   switch (act) {
     case kActRelu:
       return a > 0.f ? 1.f : 0.f;

@@ -12,9 +12,9 @@
 // the row length is no multiple of a window, row t starts `a` elements into one,
 // a = t H mod VL (VL elements a window), and window v holds the columns
 // v VL - a ... + VL - 1.  The rows of a block all have the same `a` (they lie a
-// multiple of VL rows apart).  The first and the last window of such a row hold
-// columns of its neighbours too, which are masked on reading and left alone on
-// writing.
+// multiple of VL rows apart).  The columns of such a row's first and last window,
+// which its neighbours share, are taken one by one, by the first lanes of each
+// group, with a row's lead.
 //
 // Forward: the variance is that of the centred values (no sum of squares minus
 // square of sums).  Backward: x and dy are read once; the sums of dgamma and dbeta
@@ -89,8 +89,10 @@ struct NormRing {
   static_assert(ALIGNED || PAR, "unaligned parameters are read from shared memory");
   const NormParams& p;
   int g, tid, lane, warp, a;
-  int v0;    // the thread's first window; the others follow 32 apart
-  int col0;  // its first column
+  int v0;          // the thread's first window; the others follow 32 apart
+  int col0;        // its first column
+  int v_lo, v_hi;  // the row's whole windows
+  int edge;        // the thread's column outside them, or -1
   uint64_t* bars;
   float2* red;
   uint8_t* ring;
@@ -114,6 +116,14 @@ struct NormRing {
     a = ALIGNED ? 0 : static_cast<int>(static_cast<long long>(blockIdx.x) * p.H % VL);
     v0 = warp * 32 * NW + lane;
     col0 = v0 * VL - a;
+    v_lo = a > 0 ? 1 : 0;
+    v_hi = (a + p.H) / VL;
+    edge = -1;
+    if (!ALIGNED) {
+      const int c0 = v_hi > v_lo ? v_lo * VL - a : p.H, c1 = v_hi > v_lo ? v_hi * VL - a : p.H;
+      const int j = tid < c0 ? tid : c1 + tid - c0;
+      if (j < p.H) edge = j;
+    }
     mine = smem_u32(ring) + v0 * 16;
     par[0] = smem_u32(par0 + quad(v0 * (VL / 4)));
     par[1] = smem_u32(par0 + quad(v0 * (VL / 4) + 1));
@@ -151,21 +161,20 @@ struct NormRing {
   __device__ __forceinline__ int quad(int i) const {
     return VL == 4 ? 4 * i : (i & 1) * (p.par_floats / 2) + (i >> 1) * 4;
   }
-  // A last window that ends behind the tensor (the last row's; of very short rows
-  // also some before it) is not copied.
-  __device__ __forceinline__ bool cut(long long t) const {
-    return !ALIGNED && t * p.H - a + (a + p.H + VL - 1) / VL * VL > p.T * p.H;
-  }
-  // Copies of row t into a stage, by one thread of the group.
+  // Copies of row t's whole windows into a stage, by one thread of the group.
   __device__ __forceinline__ void issue(long long t, int stage) {
-    const uint32_t windows = static_cast<uint32_t>(cut(t) ? (a + p.H) / VL : (a + p.H + VL - 1) / VL);
-    mbar_arrive_expect_tx(&bars[stage], OPS * windows * 16u);
-    if (windows != 0u) {
-      const long long at = t * p.H - a;
-      uint8_t* dst = ring + static_cast<size_t>(stage) * OPS * p.row_bytes;
-      bulk_load(dst, static_cast<const T*>(p.x) + at, windows * 16u, &bars[stage]);
-      if constexpr (OPS == 2) bulk_load(dst + p.row_bytes, static_cast<const T*>(p.dy) + at, windows * 16u, &bars[stage]);
+    const uint32_t bytes = v_hi > v_lo ? static_cast<uint32_t>(v_hi - v_lo) * 16u : 0u;
+    mbar_arrive_expect_tx(&bars[stage], OPS * bytes);
+    if (bytes != 0u) {
+      const long long at = t * p.H + v_lo * VL - a;
+      uint8_t* dst = ring + static_cast<size_t>(stage) * OPS * p.row_bytes + v_lo * 16;
+      bulk_load(dst, static_cast<const T*>(p.x) + at, bytes, &bars[stage]);
+      if constexpr (OPS == 2) bulk_load(dst + p.row_bytes, static_cast<const T*>(p.dy) + at, bytes, &bars[stage]);
     }
+  }
+  // The thread's edge column of row t of an operand (`none` without one).
+  __device__ __forceinline__ float edge_load(const void* base, long long t, float none) const {
+    return !ALIGNED && edge >= 0 && t < p.T ? op_f32(static_cast<const T*>(base)[t * p.H + edge]) : none;
   }
   __device__ __forceinline__ void bar() {
     __syncwarp();
@@ -202,43 +211,17 @@ struct NormRing {
     return make_float2(__shfl_sync(0xffffffffu, keep, 0), __shfl_sync(0xffffffffu, keep, 16));
   }
   __device__ __forceinline__ int col(int w) const { return col0 + w * 32 * VL; }  // of the thread's window w
-  __device__ __forceinline__ bool whole(int j0) const { return ALIGNED || (j0 >= 0 && j0 + VL <= p.H); }
-  __device__ __forceinline__ bool inside(int j) const { return j >= 0 && j < p.H; }
-  // window w of an operand of row t, at its shared address; columns outside the row as `none`
-  __device__ __forceinline__ void load(uint32_t addr, const void* base, long long t, int w, float none, F2* f) const {
-    op_unpack16<T>(ld_shared16(addr + w * 512), f);
-    const int j0 = col(w);
-    if (!whole(j0)) {
-      const T* row = static_cast<const T*>(base) + t * p.H;
-      const bool fetch = cut(t) && j0 + VL > p.H;
-#pragma unroll
-      for (int i = 0; i < VL; i += 2) {
-        float2 v = f2_get(f[i / 2]);
-        if (fetch) {
-          v.x = inside(j0 + i) ? op_f32(row[j0 + i]) : none;
-          v.y = inside(j0 + i + 1) ? op_f32(row[j0 + i + 1]) : none;
-        } else {
-          v.x = inside(j0 + i) ? v.x : none;
-          v.y = inside(j0 + i + 1) ? v.y : none;
-        }
-        f[i / 2] = f2(v.x, v.y);
-      }
-    }
+  // Whether the thread's window w is one of the row's whole windows.
+  __device__ __forceinline__ bool has(int w) const {
+    const int v = v0 + w * 32;
+    return (ALIGNED || v >= v_lo) && v < v_hi;
   }
+  __device__ __forceinline__ bool inside(int j) const { return j >= 0 && j < p.H; }
+  // window w of an operand at its shared address
+  __device__ __forceinline__ void load(uint32_t addr, int w, F2* f) const { op_unpack16<T>(ld_shared16(addr + w * 512), f); }
   // `out`: the thread's first column in the row
   __device__ __forceinline__ void store(T* out, int w, const F2* f) const {
-    const int j0 = col(w);
-    T* row = out - col0;
-    if (whole(j0)) {
-      *reinterpret_cast<uint4*>(out + w * 32 * VL) = op_pack16<T>(f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VL; i += 2) {
-        const float2 v = f2_get(f[i / 2]);
-        if (inside(j0 + i)) row[j0 + i] = op_from<T>(v.x);
-        if (inside(j0 + i + 1)) row[j0 + i + 1] = op_from<T>(v.y);
-      }
-    }
+    *reinterpret_cast<uint4*>(out + w * 32 * VL) = op_pack16<T>(f);
   }
   // gamma (k = 0) or beta (1) of window w: from shared memory, or (PAR false) from
   // `q` or, without one, `none`.
@@ -278,39 +261,40 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS, 1) norm_kernel(const NormPar
   uint32_t x = r.mine;
   T* out = static_cast<T*>(p.out) + r.first * p.H + r.col0;
   const long long stride = static_cast<long long>(p.walkers) * p.H;
+  const float gamma_e = !ALIGNED && r.edge >= 0 && p.gamma != nullptr ? p.gamma[r.edge] : 1.f;
+  const float beta_e = !ALIGNED && r.edge >= 0 && p.beta != nullptr ? p.beta[r.edge] : 0.f;
+  float xe_n = r.edge_load(p.x, r.first, 0.f);
   for (long long t = r.first; t < p.T; t += p.walkers) {
     // (a wait that gave up is recorded; the row's results are void)
     mbar_wait(&r.bars[s], phase, &abort_flag, kFaultNormWait);
     F2 v[NW][NP];
     float mean = 0.f;
     F2 acc = f2(0.f);
+    const float xe = xe_n;
+    xe_n = r.edge_load(p.x, t + p.walkers, 0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (r.col(w) >= p.H) continue;
-      r.load(x, p.x, t, w, 0.f, v[w]);
+      if (!r.has(w)) continue;
+      r.load(x, w, v[w]);
 #pragma unroll
       for (int i = 0; i < NP; ++i) acc = f2_add(acc, v[w][i]);
     }
     if (!p.rms) {
-      mean = r.sum(f2_sum(acc), buf) * p.inv_h;
+      mean = r.sum(f2_sum(acc) + xe, buf) * p.inv_h;
       buf ^= 1;
     }
     acc = f2(0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (r.col(w) >= p.H) continue;
+      if (!r.has(w)) continue;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         v[w][i] = f2_add(v[w][i], f2(-mean));
-        if (!r.whole(r.col(w))) {  // columns outside the row do not count
-          const float2 e = f2_get(v[w][i]);
-          const int j = r.col(w) + 2 * i;
-          v[w][i] = f2(r.inside(j) ? e.x : 0.f, r.inside(j + 1) ? e.y : 0.f);
-        }
         acc = f2_fma(v[w][i], v[w][i], acc);
       }
     }
-    const float rstd = 1.0f / sqrtf(r.sum(f2_sum(acc), buf) * p.inv_h + p.eps);
+    const float ce = !ALIGNED && r.edge >= 0 ? xe - mean : 0.f;
+    const float rstd = 1.0f / sqrtf(r.sum(fmaf(ce, ce, f2_sum(acc)), buf) * p.inv_h + p.eps);
     buf ^= 1;
     if (r.tid == 0) {
       // past the last barrier the row is in registers: its stage is filled again
@@ -319,10 +303,11 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS, 1) norm_kernel(const NormPar
       if (p.mean != nullptr) p.mean[t] = mean;
       if (p.rstd != nullptr) p.rstd[t] = rstd;
     }
+    if (!ALIGNED && r.edge >= 0) out[r.edge - r.col0] = op_from<T>(fmaf(ce * rstd, gamma_e, beta_e));
     const F2 rs = f2(rstd);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (r.col(w) >= p.H) continue;
+      if (!r.has(w)) continue;
       F2 m[NP], b[NP];
       r.param(0, p.gamma, 1.f, w, m);
 #pragma unroll
@@ -372,7 +357,13 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
     mean = p.rms ? 0.f : p.mean[r.first];
     rstd = p.rstd[r.first];
   }
+  const float gamma_e = !ALIGNED && r.edge >= 0 && p.gamma != nullptr ? p.gamma[r.edge] : 1.f;
+  float xe_n = r.edge_load(p.x, r.first, 0.f), de_n = r.edge_load(p.dy, r.first, 0.f);
+  float dg_e = 0.f, db_e = 0.f;
   for (long long t = r.first; t < p.T; t += p.walkers) {
+    const float xe = xe_n, de = de_n;
+    xe_n = r.edge_load(p.x, t + p.walkers, 0.f);
+    de_n = r.edge_load(p.dy, t + p.walkers, 0.f);
     float mean_n = 0.f, rstd_n = 0.f;
     if (t + p.walkers < p.T) {
       mean_n = p.rms ? 0.f : p.mean[t + p.walkers];
@@ -380,15 +371,15 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
     }
     // (a wait that gave up is recorded; the row's results are void)
     mbar_wait(&r.bars[s], phase, &abort_flag, kFaultNormWait);
-    // xh = x rstd - mean rstd; outside the row x = mean, dy = 0
+    // xh = x rstd - mean rstd
     const F2 rs = f2(rstd), shift = f2(-mean * rstd);
     F2 a1 = f2(0.f), a2 = f2(0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (r.col(w) >= p.H) continue;
+      if (!r.has(w)) continue;
       F2 v[NP], d[NP], m[NP];
-      r.load(x, p.x, t, w, mean, v);
-      r.load(x + r.op_b, p.dy, t, w, 0.f, d);
+      r.load(x, w, v);
+      r.load(x + r.op_b, w, d);
       r.param(0, p.gamma, 1.f, w, m);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -399,7 +390,15 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
         a2 = f2_fma(e, m[i], a2);
       }
     }
-    float keep = r.sum2_put(f2_sum(a1), f2_sum(a2), buf);
+    float e1 = 0.f, e2 = 0.f;
+    if (!ALIGNED && r.edge >= 0) {
+      const float e = de * fmaf(xe, rstd, -mean * rstd);
+      dg_e += e;
+      db_e += de;
+      e1 = de * gamma_e;
+      e2 = e * gamma_e;
+    }
+    const float keep = r.sum2_put(f2_sum(a1) + e1, f2_sum(a2) + e2, buf);
     r.bar();
     const float2 sums = r.sum2_get(keep, buf);
     buf ^= 1;
@@ -410,13 +409,15 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
     }
     // dx = rstd (dy gamma - s1 - xh s2) = (rstd gamma) dy + k1 x + k0
     const float s1 = p.rms ? 0.f : sums.x * p.inv_h, s2 = sums.y * p.inv_h;
-    const F2 k1 = f2(-rstd * rstd * s2), k0 = f2(-rstd * fmaf(s2, -mean * rstd, s1));
+    const float k1e = -rstd * rstd * s2, k0e = -rstd * fmaf(s2, -mean * rstd, s1);
+    const F2 k1 = f2(k1e), k0 = f2(k0e);
+    if (!ALIGNED && r.edge >= 0) out[r.edge - r.col0] = op_from<T>(fmaf(de, gamma_e * rstd, fmaf(xe, k1e, k0e)));
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (r.col(w) >= p.H) continue;
+      if (!r.has(w)) continue;
       F2 v[NP], d[NP], m[NP];
-      r.load(x, p.x, t, w, mean, v);
-      r.load(x + r.op_b, p.dy, t, w, 0.f, d);
+      r.load(x, w, v);
+      r.load(x + r.op_b, w, d);
       r.param(0, p.gamma, 1.f, w, m);
 #pragma unroll
       for (int i = 0; i < NP; ++i) d[i] = f2_fma(d[i], f2_mul(m[i], rs), f2_fma(v[i], k1, k0));
@@ -446,21 +447,22 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
     acc = reinterpret_cast<float*>(norm_smem + norm_head(p.groups)) + p.par_floats + static_cast<size_t>(r.g) * 2 * p.H;
   }
 #pragma unroll
-  for (int w = 0; w < NW; ++w)
+  for (int w = 0; w < NW; ++w) {
+    if (!r.has(w)) continue;
 #pragma unroll
     for (int i = 0; i < VL; i += 2) {
       const int j = r.col(w) + i;
       const float2 e = f2_get(dg[w][i / 2]), d = f2_get(db[w][i / 2]);
       if (ALIGNED) {
-        if (j < p.H) {
-          *reinterpret_cast<float2*>(acc + j) = e;
-          *reinterpret_cast<float2*>(acc + p.H + j) = d;
-        }
+        *reinterpret_cast<float2*>(acc + j) = e;
+        *reinterpret_cast<float2*>(acc + p.H + j) = d;
       } else {
-        if (r.inside(j)) acc[j] = e.x, acc[p.H + j] = d.x;
-        if (r.inside(j + 1)) acc[j + 1] = e.y, acc[p.H + j + 1] = d.y;
+        acc[j] = e.x, acc[p.H + j] = d.x;
+        acc[j + 1] = e.y, acc[p.H + j + 1] = d.y;
       }
     }
+  }
+  if (!ALIGNED && r.edge >= 0) acc[r.edge] = dg_e, acc[p.H + r.edge] = db_e;
   if (p.groups > 1) {
     __syncthreads();
     const float* all = reinterpret_cast<const float*>(norm_smem + norm_head(p.groups)) + p.par_floats;

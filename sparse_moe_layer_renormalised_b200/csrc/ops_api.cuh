@@ -19,6 +19,22 @@ bool ws_fits(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws != nullptr && (reinterpret_cast<uintptr_t>(ws) % kAlign) == 0 && have >= need);
 }
 
+// SMs of the current device, asked for once.
+int op_sms() {
+  static int cache[128] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return num_sms();
+  if (cache[dev] == 0) cache[dev] = num_sms();
+  return cache[dev];
+}
+
+// Allows a kernel `smem` bytes of dynamic shared memory (at every call: what was
+// allowed goes with the device's context).
+template <typename K>
+cudaError_t op_allow_smem(K kern, size_t smem) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+}
+
 // Launches a kernel so that it may be set up before the one ahead of it in the
 // stream has ended (its pdl_wait() waits for that); `cluster` CTAs a cluster.
 template <typename K, typename... A>
@@ -146,13 +162,13 @@ NormPlan norm_plan(const moe_norm_desc& d, bool backward) {
   if (q.nw > 4 && vl == 4 && q.nw < 8) q.nw = 8;  // (fewer variants)
   q.tpg = static_cast<int>(cdiv(windows, 32 * q.nw) * 32);
   q.groups = std::max(1, std::min(q.tpg > 32 ? 14 : 32, threads / q.tpg));
-  q.groups = static_cast<int>(std::max<long long>(1, std::min<long long>(q.groups, cdiv(d.T, num_sms()))));
+  q.groups = static_cast<int>(std::max<long long>(1, std::min<long long>(q.groups, cdiv(d.T, op_sms()))));
   q.row_bytes = windows * 16;
   // gamma and beta in shared memory, unless rows of whole windows are so long that
   // they would leave less than two stages, or so few that no group takes a second one
   const size_t par_bytes = static_cast<size_t>(windows) * vl * (backward ? 4 : 8);
   if (!norm_aligned(d) || (par_bytes + 2 * static_cast<size_t>(ops) * q.row_bytes <= 224 * 1024 &&
-                           d.T > static_cast<long long>(q.groups) * num_sms()))
+                           d.T > static_cast<long long>(q.groups) * op_sms()))
     q.par_floats = windows * vl;
   // three stages at least are worth a group
   for (;; --q.groups) {
@@ -162,7 +178,7 @@ NormPlan norm_plan(const moe_norm_desc& d, bool backward) {
     q.smem = head + std::max<size_t>(group * q.stages, backward && q.groups > 1 ? static_cast<size_t>(q.groups) * d.H * 8 : 0);
     if (q.stages >= 3 || q.groups <= 2) break;
   }
-  q.blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(cdiv(d.T, q.groups), num_sms())));
+  q.blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(cdiv(d.T, q.groups), op_sms())));
   // the rows of a block start at one offset in a window: they lie as many rows apart
   // as there are blocks, a multiple of a window's elements (or are one a block)
   if (!norm_aligned(d) && d.T > q.blocks) q.blocks = std::max(vl, q.blocks - q.blocks % vl);
@@ -171,8 +187,7 @@ NormPlan norm_plan(const moe_norm_desc& d, bool backward) {
 
 template <typename K>
 moe_status norm_launch(K kern, const NormParams& p, const NormPlan& q, cudaStream_t s) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(q.smem)) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  if (op_allow_smem(kern, q.smem) != cudaSuccess) return MOE_ERR_CUDA;
   return op_launch(kern, q.blocks, q.tpg * q.groups, q.smem, s, 0, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -299,7 +314,7 @@ LinWidePlan lin_wide_plan(long long Q, long long P, int nkb, int pairs) {
 }
 
 // Bytes for the partial sums of a last wave, whatever the plan: one tile a pair.
-size_t lin_wide_ws() { return static_cast<size_t>(num_sms() / 2) * 256 * 256 * 4; }
+size_t lin_wide_ws() { return static_cast<size_t>(op_sms() / 2) * 256 * 256 * 4; }
 
 // Few rows, or fewer tiles than would keep half the pairs at work even in parts:
 // the skinny kernel.
@@ -310,7 +325,7 @@ bool lin_is_skinny(long long Q, long long P) {
 template <typename OutT>
 cudaError_t lin_launch_wide(const LinProblem& g, LinParams& p, cudaStream_t s) {
   auto kern = linear_wide_kernel<OutT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(LW_SMEM));
+  cudaError_t e = op_allow_smem(kern, LW_SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(LW_THREADS);
@@ -324,7 +339,7 @@ cudaError_t lin_launch_wide(const LinProblem& g, LinParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   static int pairs_cache[128] = {};
   const int pairs = cluster_pairs(kern, cfg, pairs_cache);
-  const LinWidePlan w = lin_wide_plan(g.Q, g.P, p.nkb, std::min(pairs, num_sms() / 2));
+  const LinWidePlan w = lin_wide_plan(g.Q, g.P, p.nkb, std::min(pairs, op_sms() / 2));
   p.bn = w.bn;
   p.q_tiles = w.q_tiles;
   p.p_tiles = w.p_tiles;
@@ -350,8 +365,7 @@ template <typename OutT, int BN, bool QMN>
 cudaError_t lin_launch_skinny_inst(const LinProblem& g, LinParams& p, cudaStream_t s) {
   using C = LsCfg<BN, QMN>;
   auto kern = linear_skinny_kernel<OutT, BN, QMN>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  cudaError_t e = op_allow_smem(kern, C::kSmem);
   if (e != cudaSuccess) return e;
   p.bn = BN;
   p.p_tiles = static_cast<int>(cdiv(g.P, 128));
@@ -361,7 +375,7 @@ cudaError_t lin_launch_skinny_inst(const LinProblem& g, LinParams& p, cudaStream
   // 15.9 us at 4 x 7168 x 3584), each with a few blocks of it
   const long long tiles = static_cast<long long>(p.p_tiles) * p.q_tiles;
   const int split = static_cast<int>(
-      std::max<long long>(1, std::min<long long>({LS_MAX_SPLIT, 16LL * num_sms() / 10 / tiles, p.nkb / 2})));
+      std::max<long long>(1, std::min<long long>({LS_MAX_SPLIT, 16LL * op_sms() / 10 / tiles, p.nkb / 2})));
   LinMaps maps;
   std::memset(&maps, 0, sizeof maps);
   if (!lin_map(&maps.p, g.p, g.p_mn, g.P, g.R, 128) || !lin_map(&maps.q, g.q, g.q_mn, g.Q, g.R, BN))
@@ -403,7 +417,7 @@ moe_status lin_product_of(int out_type, const LinProblem& g, const LinParams& p,
 // Blocks along the rows of the dp kernel: about eight a SM in all.
 long long lin_dp_parts(const moe_linear_desc& d) {
   const long long across = cdiv(d.N, LIN_DP_THREADS * 8);
-  return std::max<long long>(1, std::min<long long>({d.M, cdiv(8LL * num_sms(), across), 65535}));
+  return std::max<long long>(1, std::min<long long>({d.M, cdiv(8LL * op_sms(), across), 65535}));
 }
 size_t lin_dp_bytes(const moe_linear_desc& d) {
   return d.act == MOE_ACT_NONE ? 0 : round_up(static_cast<size_t>(d.M) * d.N * 2, kAlign);
@@ -426,9 +440,9 @@ bool clip_list_ok(const moe_grad_tensor* list, int32_t count) {
   return true;
 }
 
-// Launches over the list and blocks of each.
+// Launches over the list, and the most blocks of each.
 int clip_launches(int32_t count) { return std::max(1, static_cast<int>(cdiv(count, CLIP_MAX))); }
-int clip_blocks() { return 8 * num_sms(); }
+int clip_blocks() { return 8 * op_sms(); }
 
 // 16-byte vectors that a tensor touches.
 long long clip_vectors(const moe_grad_tensor& t) {
@@ -436,20 +450,22 @@ long long clip_vectors(const moe_grad_tensor& t) {
   return cdiv((t.n + skew) * es, 16);
 }
 
-// Vectors of a chunk: 64 KB, or one round of a block's loads (32 KB) where the whole
-// list would not give every block a few.
+// Vectors of a chunk: 64 KB, halved down to 8 KB while the whole list would not give
+// every block one.
 int clip_chunk_vectors(const moe_grad_tensor* list, int32_t count) {
   long long total = 0;
   for (int i = 0; i < count; ++i)
     if (list[i].n > 0) total += clip_vectors(list[i]);
-  constexpr int kRound = CLIP_LOADS * CLIP_THREADS;
-  return total >= 8LL * kRound * clip_blocks() ? 2 * kRound : kRound;
+  int chunk = 2 * CLIP_LOADS * CLIP_THREADS;
+  while (chunk > 2 * CLIP_THREADS && total < static_cast<long long>(chunk) * clip_blocks()) chunk /= 2;
+  return chunk;
 }
 
 template <int MAXT>
 moe_status clip_run(const moe_grad_tensor* list, int32_t count, bool max_norm_kind, float max_norm, float* norm_out,
                     double* partial, cudaStream_t s) {
-  const int nl = clip_launches(count), blocks = clip_blocks();
+  const int nl = clip_launches(count);
+  int parts = 0;  // partial sums written by the first pass
   const int chunk = clip_chunk_vectors(list, count);
   for (int pass = 0; pass < 2; ++pass) {
     for (int li = 0; li < nl; ++li) {
@@ -471,14 +487,15 @@ moe_status clip_run(const moe_grad_tensor* list, int32_t count, bool max_norm_ki
       if (chunks > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED;
       l.chunks = static_cast<int>(chunks);
       cudaError_t e;
+      const int grid = std::max(1, std::min(clip_blocks(), l.chunks));
       if (pass == 0) {
-        e = op_launch(max_norm_kind ? clip_norm_kernel<MAXT, true> : clip_norm_kernel<MAXT, false>, blocks, CLIP_THREADS, 0, s,
-                      0, l, partial + li * blocks);
+        e = op_launch(max_norm_kind ? clip_norm_kernel<MAXT, true> : clip_norm_kernel<MAXT, false>, grid, CLIP_THREADS, 0, s,
+                      0, l, partial + parts);
+        parts += grid;
       } else {
         float* out = li == 0 ? norm_out : nullptr;
-        const int grid = std::max(1, std::min(blocks, l.chunks));
         e = op_launch(max_norm_kind ? clip_scale_kernel<MAXT, true> : clip_scale_kernel<MAXT, false>, grid, CLIP_THREADS, 0, s,
-                      0, l, static_cast<const double*>(partial), nl * blocks, max_norm, out);
+                      0, l, static_cast<const double*>(partial), parts, max_norm, out);
       }
       if (e != cudaSuccess) return MOE_ERR_CUDA;
     }

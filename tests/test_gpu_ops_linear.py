@@ -88,6 +88,41 @@ def test_non_finite_rows_stay_alone():
     assert bad.nonzero().view(-1).tolist() == [3, 9]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ACTS)
+def test_activations_far_out(act, dtype):
+    """Pre-activations from 0 to the type's largest, and the slopes there."""
+    big = 6e4 if dtype == "f16" else 1e30
+    v = torch.tensor([0.0, 1e-4, 0.5, 3.0, 8.0, 12.0, 20.0, 88.0, 89.0, 100.0, 104.0, 1000.0, big, -0.0, -1e-4, -0.5, -3.0,
+                      -8.0, -12.0, -20.0, -88.0, -89.0, -100.0, -104.0, -1000.0, -big]).to(DT[dtype])
+    n, N = v.numel(), 64
+    x, eye = torch.zeros(n, N, dtype=DT[dtype]), torch.eye(N).to(DT[dtype])
+    x[torch.arange(n), torch.arange(n)] = v
+    for rows in (n, 2600):  # a few rows, and enough for the wide tiles (of a wider product)
+        cols = N if rows == n else 1024
+        w = torch.zeros(cols, N, dtype=DT[dtype])
+        w[:N] = eye
+        xx = x.repeat(-(-rows // n), 1)[:rows].contiguous()
+        y = torch.empty(rows, cols, dtype=DT[dtype], device="cuda")
+        pre = torch.empty_like(y)
+        assert _linear(moe.linear_desc(rows, cols, N, act, dtype), xx.cuda(), w.cuda(), None, None, pre, y) == moe.MOE_OK
+        at = torch.arange(rows), torch.arange(rows) % n
+        want = oo.act(xx[at].double(), act)
+        tol = want.abs() * (HALF[dtype] + 2.0 ** -18) + 2.0 ** -19 * xx[at].double().abs().clamp_max(30.0) + TINY[dtype]
+        within(y[at], want, tol, act)
+        # the slope: dW of a product with one row of ones is dp itself
+    dy = torch.ones(1, n, dtype=DT[dtype])
+    d = moe.linear_desc(1, -(-n // 8) * 8, 8, act, dtype)
+    pad = d.N - n
+    p1 = torch.cat([v, torch.zeros(pad, dtype=DT[dtype])]).view(1, -1)
+    dy = torch.ones(1, d.N, dtype=DT[dtype])
+    db = torch.empty(d.N, device="cuda")
+    ws = workspace(moe.moe_linear_backward_workspace_size(d))
+    assert moe.moe_linear_backward(d, dy.cuda(), p1.cuda(), None, None, None, None, db, ws) == moe.MOE_OK
+    want = oo.act_grad(p1[0].double().clamp(-1e3, 1e3), act) if act != "none" else torch.ones(d.N, dtype=torch.float64)
+    within(db, want, 2.0 ** -18 * torch.ones_like(want) * (1.0 + p1[0].double().abs().clamp_max(10.0)), act + "'")
+
+
 def _check_backward(M, N, K, dtype, act, need=(True, True, True)):
     x, w, b, dy = _data(M, N, K, dtype, M + N + 7 * K)
     dy = dy.to(DT[dtype])
