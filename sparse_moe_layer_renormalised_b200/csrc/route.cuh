@@ -1,8 +1,9 @@
 // Routing from logits: scores (softmax or sigmoid), selection bias, groups,
 // top-k in the exact order of the keys, weights; and the weights' gradient.
 //
-// Forward: one warp per token, its row of at most 1024 logits in registers.
-// What bounds it is instruction issue next to the one read of the logits, so
+// Forward: one warp per token, its row of at most 1024 logits in registers.  (Many
+// short rows: route_short.cuh.)  What bounds it is instruction issue next to the one
+// read of the logits (16384 x 896 fp32, sigmoid + bias, top 16: 27 us, 59 MB in 9), so
 // the top-k does not run k arg-max rounds over all keys: the k-th largest of
 // the 32 lanes' own maxima (one 32-wide sort) is a lower bound of the k-th key,
 // and only the few keys at or above it (22 of 896 at k = 16, on average) are
@@ -292,15 +293,14 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 8) route_kernel(const RouteP
   uint16_t* cand = reinterpret_cast<uint16_t*>(smem + ROUTE_LISTS);
   float* val = reinterpret_cast<float*>(smem + ROUTE_LISTS);
 
-  // logits; NaN as -inf, also where the row ends
+  // logits, -inf where the row ends (a NaN is below every number in the comparisons
+  // and maxima below)
   float key[NV];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int e0 = (c * 32 + lane) * VL;
     if (e0 < E) {
       op_load<T, VL>(row + e0, key + c * VL);
-#pragma unroll
-      for (int i = 0; i < VL; ++i) key[c * VL + i] = fmaxf(key[c * VL + i], -INFINITY);
     } else {
 #pragma unroll
       for (int i = 0; i < VL; ++i) key[c * VL + i] = -INFINITY;
@@ -310,7 +310,10 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 8) route_kernel(const RouteP
   const bool need_scores = biased || (grouped && p.gtop == 2);
   if (p.softmax && (need_scores || !p.renorm)) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
+    for (int i = 0; i < NV; ++i) {
+      key[i] = fmaxf(key[i], -INFINITY);  // NaN as masked
+      m = fmaxf(m, key[i]);
+    }
     m = warp_max(m);
     float z4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

@@ -188,6 +188,62 @@ def test_many_rows(score, E, k, groups, keep, group_top):
             assert int((idx.long() != want).any(1).sum()) == 0, (seed, bias is None)
 
 
+def _special_rows(E, seed):
+    """Rows with nothing left, little left, NaN, infinities, ties, saturated and usual logits."""
+    l = _logits(26, E, seed)
+    l[0] = -INF
+    l[1] = math.nan
+    l[2, ::2] = -INF
+    l[3, E // 20:] = -INF
+    l[4] = -INF
+    l[4, E - 1] = 0.3
+    l[5, :E * 3 // 4] = math.nan
+    l[6] = torch.finfo(torch.float32).min
+    l[7, E // 9:] = torch.finfo(torch.float32).min
+    l[8, ::3] = math.nan
+    l[9, E // 3] = INF
+    l[10, E // 3] = INF
+    l[10, E // 30] = INF
+    l[11] = 0.0
+    l[12] = -0.0
+    l[12, ::2] = 0.0
+    l[13] = 80.0
+    l[14] = -80.0
+    l[15] = -200.0
+    l[16] = torch.randint(0, 3, (E,), generator=torch.Generator().manual_seed(seed)).float()
+    return l
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,k,groups,keep,group_top", [
+    (128, 8, 1, 1, 1), (127, 5, 1, 1, 1), (64, 6, 1, 1, 1), (61, 8, 1, 1, 1), (96, 12, 1, 1, 1), (125, 16, 1, 1, 1),
+    (96, 12, 4, 2, 2), (128, 8, 8, 4, 2), (128, 16, 32, 9, 2), (66, 7, 11, 5, 1), (60, 10, 3, 2, 2), (32, 8, 32, 8, 1),
+    (8, 8, 1, 1, 1), (3, 2, 1, 1, 1), (1, 1, 1, 1, 1)])
+def test_many_short_rows(score, dtype, E, k, groups, keep, group_top):
+    """More rows than the GPU holds warps: several tokens a warp, usual and special ones side by side, and a last
+    warp with a part of them."""
+    warps = 32 * torch.cuda.get_device_properties(0).multi_processor_count
+    b = _bias(E, E)
+    odd = b.clone()
+    odd[0] = -INF
+    odd[E // 2] = math.nan
+    odd[E - 1] = INF
+    for i, bias in enumerate((None, b, torch.zeros(E), odd, 0.75)):
+        l = _special_rows(E, E + k)
+        if isinstance(bias, float):  # keys within 2^-24 of one value in the last row
+            bias = (bias - oo.scores(l[25:], score)[0]).to(torch.float32)
+        n, T = l.shape[0], warps + 5
+        at = torch.arange(T) * 7 % n
+        kw = dict(score=score, groups=groups, group_top=group_top, renorm=i != 1, scale=1.0 if i else 2.5)
+        l_, idx, w = _run(l[at], bias, k, dtype, keep_groups=keep, **kw)
+        want_idx, want_w = oo.route(l.to(DT[dtype]), bias, k, keep=keep, **kw)
+        want_idx, want_w = want_idx[at], want_w[at]
+        assert torch.equal(idx, want_idx), (i, (idx != want_idx).any(1).nonzero().view(-1)[:8].tolist())
+        within(w, want_w, want_w.abs() * _rel(l_) + 1e-37, "weights")
+    assert moe.moe_device_error() == (moe.MOE_OK, 0)
+
+
 def test_deterministic_and_rows_independent():
     l = _logits(300, 896, 1)
     b = _bias(896, 2)
