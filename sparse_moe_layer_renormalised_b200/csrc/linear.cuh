@@ -55,28 +55,71 @@ __host__ __device__ constexpr uint32_t lin_idesc(int M, int N, bool bf16, bool a
 
 enum LinAct : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-__device__ __forceinline__ float rcp_approx(float x) {
+// Hardware reciprocal (within 1 ulp) and 2^x (within 2 ulp + that of x); results
+// below 2^-126 are 0.
+__device__ __forceinline__ float rcp_fast(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2E = 1.4426950408889634f;
 
-// sigmoid by the fast exponential and reciprocal: relative error below 2^-23 (4 + 1.2 |a|).
-__device__ __forceinline__ float lin_sigmoid(float a) { return rcp_approx(1.0f + __expf(-a)); }
+// sigmoid: relative error below 2^-23 (4 + 1.2 |a|); 0 below a = -87.3 (the value is
+// under 2^-126 there).
+__device__ __forceinline__ float lin_sigmoid(float a) { return rcp_fast(1.0f + ex2_fast(-kLog2E * a)); }
 
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
 
 // erfc(|a| / sqrt 2) as e^(-a^2 / 2) times a polynomial in t = 1 / (1 + 0.3275911 x),
 // x = |a| / sqrt 2 (Abramowitz and Stegun, Handbook of Mathematical Functions,
 // 7.1.26; absolute error 1.5e-7): a third of erff's instructions, and no branch.
+constexpr float kErfcX = 0.3275911f * 0.7071067811865476f;
+constexpr float kErfc0 = 0.254829592f, kErfc1 = -0.284496736f, kErfc2 = 1.421413741f, kErfc3 = -1.453152027f, kErfc4 = 1.061405429f;
 // *e receives the exponential.
 __device__ __forceinline__ float lin_erfc_abs(float a, float* e) {
-  const float x = fabsf(a) * 0.7071067811865476f;
-  const float t = rcp_approx(fmaf(0.3275911f, x, 1.0f));
-  *e = __expf(-x * x);
-  const float q = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t, 0.254829592f);
+  const float t = rcp_fast(fmaf(kErfcX, fabsf(a), 1.0f));
+  *e = ex2_fast(a * (a * (-0.5f * kLog2E)));
+  const float q = fmaf(fmaf(fmaf(fmaf(kErfc4, t, kErfc3), t, kErfc2), t, kErfc1), t, kErfc0);
   return q * t * *e;
 }
+
+// a Phi(a) = max(a, 0) - |a| erfc(|a| / sqrt 2) / 2, on both sides of 0, of two values
+// at once (nine instructions a value: what the epilogue's warps issue beside the
+// product's is seen in its time).  Beyond 100 erfc is 0, and no infinity meets it; a
+// NaN stays one.
+__device__ __forceinline__ void lin_gelu2(float& a, float& b) {
+  const F2 v = f2(a, b);
+  const F2 t = f2(rcp_fast(fmaf(kErfcX, fabsf(a), 1.0f)), rcp_fast(fmaf(kErfcX, fabsf(b), 1.0f)));
+  const float2 x = f2_get(f2_mul(v, f2_mul(v, f2(-0.5f * kLog2E))));
+  const F2 e = f2(ex2_fast(x.x), ex2_fast(x.y));
+  F2 q = f2(-0.5f * kErfc4);
+  q = f2_fma(q, t, f2(-0.5f * kErfc3));
+  q = f2_fma(q, t, f2(-0.5f * kErfc2));
+  q = f2_fma(q, t, f2(-0.5f * kErfc1));
+  q = f2_fma(q, t, f2(-0.5f * kErfc0));
+  q = f2_mul(f2_mul(q, t), e);
+  const float2 y = f2_get(f2_fma(f2(fminf(fabsf(a), 100.f), fminf(fabsf(b), 100.f)), q, f2(fmaxf(a, 0.f), fmaxf(b, 0.f))));
+  a = y.x;
+  b = y.y;
+}
+
+// a sigmoid(a (k1 + k2 a^2)) of two values at once: silu with k = (1, 0), and gelu's tanh
+// form, (1 + tanh u) / 2 being sigmoid(2 u).
+__device__ __forceinline__ void lin_gate2(float& a, float& b, float k1, float k2) {
+  const F2 v = f2(a, b);
+  const F2 k = k2 == 0.f ? f2(-kLog2E * k1) : f2_fma(f2_mul(v, v), f2(-kLog2E * k2), f2(-kLog2E * k1));
+  const float2 x = f2_get(f2_mul(v, k));
+  const float2 d = f2_get(f2_add(f2(ex2_fast(x.x), ex2_fast(x.y)), f2(1.f)));
+  const float2 y = f2_get(f2_mul(v, f2(rcp_fast(d.x), rcp_fast(d.y))));
+  a = y.x;
+  b = y.y;
+}
+constexpr float kTanh1 = 2.f * kSqrt2OverPi, kTanh2 = kTanh1 * 0.044715f;
 
 __device__ __forceinline__ float lin_act(float a, int act) {
   switch (act) {
@@ -85,14 +128,15 @@ __device__ __forceinline__ float lin_act(float a, int act) {
     case kActSilu:
       return a * lin_sigmoid(a);
     case kActGelu: {
-      // a Phi(a) = max(a, 0) - |a| erfc(|a| / sqrt 2) / 2 on both sides of 0
-      float e;
-      const float c = lin_erfc_abs(a, &e);
-      // (beyond 100 c is 0: no product of an infinity with it)
-      return a == a ? fmaf(-0.5f * fminf(fabsf(a), 100.f), c, fmaxf(a, 0.f)) : a;
+      float other = 0.f;
+      lin_gelu2(a, other);
+      return a;
     }
-    case kActGeluTanh:  // (1 + tanh u) / 2 = sigmoid(2 u)
-      return a * lin_sigmoid(2.f * kSqrt2OverPi * (a + 0.044715f * a * a * a));
+    case kActGeluTanh: {
+      float other = 0.f;
+      lin_gate2(a, other, kTanh1, kTanh2);
+      return a;
+    }
     default:
       return a;
   }
@@ -226,6 +270,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+__device__ __forceinline__ void lin_add2(float& a, float& b, F2 c) {
+  const float2 y = f2_get(f2_add(f2(a, b), c));
+  a = y.x;
+  b = y.y;
+}
+
 // The activation of 32 values, chosen once.
 __device__ __forceinline__ void lin_act32(float (&a)[32], int act) {
   switch (act) {
@@ -237,15 +287,15 @@ __device__ __forceinline__ void lin_act32(float (&a)[32], int act) {
       break;
     case kActSilu:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) a[i] = lin_act(a[i], kActSilu);
+      for (int i = 0; i < 32; i += 2) lin_gate2(a[i], a[i + 1], 1.f, 0.f);
       break;
     case kActGelu:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) a[i] = lin_act(a[i], kActGelu);
+      for (int i = 0; i < 32; i += 2) lin_gelu2(a[i], a[i + 1]);
       break;
     default:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) a[i] = lin_act(a[i], kActGeluTanh);
+      for (int i = 0; i < 32; i += 2) lin_gate2(a[i], a[i + 1], kTanh1, kTanh2);
   }
 }
 
@@ -515,10 +565,8 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
               for (int i = 0; i < 32; i += 4) {
                 if (col + i < p.P) {
                   const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col + i));
-                  a[i] += b.x;
-                  a[i + 1] += b.y;
-                  a[i + 2] += b.z;
-                  a[i + 3] += b.w;
+                  lin_add2(a[i], a[i + 1], f2(b.x, b.y));
+                  lin_add2(a[i + 2], a[i + 3], f2(b.z, b.w));
                 }
               }
             }
@@ -532,10 +580,10 @@ __global__ void __launch_bounds__(LW_THREADS, 1)
             for (int j = 0; j < 4; ++j) {
               uint4* at = reinterpret_cast<uint4*>(box + ((j ^ swz) << 4));
               if (has_res) {
-                float r[8];
+                F2 r[4];
                 op_unpack16<OutT>(*at, r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a[8 * j + i] += r[i];
+                for (int i = 0; i < 4; ++i) lin_add2(a[8 * j + 2 * i], a[8 * j + 2 * i + 1], r[i]);
               }
               *at = op_pack16<OutT>(a + 8 * j);
             }
