@@ -6,7 +6,9 @@
 // several rows ahead, so that loads stay in flight while a row's sums are formed
 // and its barriers waited for.  (A block per row with the row in registers leaves
 // the memory idle there: 16384 x 7168 bf16 took 115 us forward against 71 for its
-// bytes.)  A thread has the same columns in all of its rows.
+// bytes.)  A thread has the same columns in all of its rows.  Layer norm of 16384 x 7168
+// bf16: 91 us forward, 124 us backward (5.2 and 5.7 TB/s; a copy reaches 6.6); RMS norm
+// of 4097 x 5001 fp16: 20 and 43 us.
 //
 // Rows are read and written in 16-byte windows of the memory they lie in: where
 // the row length is no multiple of a window, row t starts `a` elements into one,

@@ -337,10 +337,13 @@ LinWidePlan lin_wide_plan(long long Q, long long P, int nkb, int pairs) {
 // Bytes for the partial sums of a last wave, whatever the plan: one tile a pair.
 size_t lin_wide_ws() { return static_cast<size_t>(op_sms() / 2) * 256 * 256 * 4; }
 
-// Few rows, or fewer tiles than would keep half the pairs at work even in parts:
-// the skinny kernel.
+// The skinny kernel for few rows (bf16, skinny against wide: 32 x 7168 x 3584 13.4 and 22.7
+// us, 128 rows 17.0 and 23.5, 160 rows 22.5 and 23.8, 512 rows 36 and 28.6), and for
+// outputs whose 128 x 128 tiles take half of the SMs at most: it splits their sums
+// over several CTAs (1024 x 896 x 7168 20.7 and 22.5, 1024 x 1024 x 1024 10.6 and 13.3; 1024
+// x 2048 x 2048, 128 tiles, 23.4 and 20.4).
 bool lin_is_skinny(long long Q, long long P) {
-  return Q <= 128 || cdiv(Q, 256) * cdiv(P, 256) < 8;
+  return Q <= 128 || cdiv(Q, 128) * cdiv(P, 128) <= op_sms() / 2;
 }
 
 template <typename OutT>
