@@ -66,6 +66,16 @@ __device__ __forceinline__ float route_tol(int softmax, float smax, float key) {
   return (softmax ? 3e-6f : 4e-7f) * smax + 7e-8f * fabsf(key);
 }
 
+// Bound of the error of a group's score in fp32, key a or the sum of keys a and b
+// (b -inf: a alone), with the bound taken off it or added.  Each key's error goes
+// with its own size, which may be far above the sum's: route_tol's 7e-8 for each,
+// once more for the sum's rounding, and once for that of score - bound.
+__device__ __forceinline__ float route_group_tol(int softmax, float smax, float a, float b) {
+  const bool two = b != -INFINITY;
+  const float keys = fabsf(a) + (two ? fabsf(b) : 0.f), sum = fabsf(two ? a + b : a);
+  return fminf((two ? 2.f : 1.f) * (softmax ? 3e-6f : 4e-7f) * smax + 7e-8f * (keys + 2.f * sum), FLT_MAX);
+}
+
 // e^(l - m) over the row's maximum m; the limit where m is infinite.
 __device__ __forceinline__ float route_exp(float l, float m) {
   if (isinf(m)) return l == m && m > 0.f ? 1.f : 0.f;
@@ -400,16 +410,18 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 8) route_kernel(const RouteP
       b = fmaxf(fmaxf(b, ob), fminf(a, oa));
       a = fmaxf(a, oa);
     }
-    float score = p.gtop == 2 && b != -INFINITY ? a + b : a;
+    if (p.gtop == 1) b = -INFINITY;
+    float score = b != -INFINITY ? a + b : a;
     score = __shfl_sync(0xffffffffu, score, (lane * lpg) & 31);
     if (lane >= p.groups) score = -INFINITY;
     kept = route_keep(score, p.groups, p.keep, lane);
     if (need_scores) {
+      // the least that a kept group may have against the most of one left out
+      const float tol = __shfl_sync(0xffffffffu, route_group_tol(p.softmax, smax, a, b), (lane * lpg) & 31);
       const bool mine = (kept >> lane) & 1u;
-      const float lo = -warp_max(mine ? -score : -INFINITY);
-      const float hi = warp_max(mine || lane >= p.groups ? -INFINITY : score);
-      const float tol = p.gtop * (route_tol(p.softmax, smax, lo) + route_tol(p.softmax, smax, hi));
-      if (hi != -INFINITY && !(lo - hi > tol)) {
+      const float lo = -warp_max(mine ? tol - score : -INFINITY);
+      const float hi = warp_max(mine || score == -INFINITY ? -INFINITY : score + tol);
+      if (hi != -INFINITY && !(lo > hi)) {
         if (p.softmax) z64 = route_sum64(row, E, m, lane);
         kept = route_keep64<T>(p, row, val, smax, m, z64, lane, lpg);
       }

@@ -16,7 +16,7 @@
 namespace moe {
 
 // Shared memory of a token: E + 2 sort keys (or, before them, the keys that the groups
-// are ranked by), the numbers of the listed experts, and 144 bytes for 32 group scores
+// are ranked by and the bounds of the groups' scores), the numbers of the listed experts, and 144 bytes for 32 group scores
 // or, after them, the chosen keys.  Tokens lie 16 bytes off a multiple of 128 apart:
 // their lanes read different banks.
 __host__ __device__ constexpr int route_short_cand(int E) { return ((E + 2) * 8 + 15) / 16 * 16; }
@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 7) route_short_kernel(const 
   uint8_t* const mem = smem + sub * token_bytes;
   unsigned long long* const list = reinterpret_cast<unsigned long long*>(mem);
   float* const val = reinterpret_cast<float*>(mem);
+  float* const gtol = val + E;  // (at most E groups)
   float* const gscore = reinterpret_cast<float*>(mem + route_short_tail(E));
   unsigned long long* const chosen = reinterpret_cast<unsigned long long*>(gscore);
   uint16_t* const cand = reinterpret_cast<uint16_t*>(mem + route_short_cand(E));
@@ -192,7 +193,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 7) route_short_kernel(const 
         a = fmaxf(a, v);
         if (++j == p.gsize) j = 0;
       }
-      gscore[g] = p.gtop == 2 && b != -INFINITY ? a + b : a;
+      if (p.gtop == 1) b = -INFINITY;
+      gscore[g] = b != -INFINITY ? a + b : a;
+      gtol[g] = route_group_tol(p.softmax, smax, a, b);
     }
     __syncwarp();
     // equal scores go to the lower group
@@ -205,11 +208,12 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 7) route_short_kernel(const 
         const float so = gscore[o];
         rank += (so > score || (so == score && o < g)) ? 1 : 0;
       }
+      // the least that a kept group may have, the most of one left out
       if (rank < p.keep) {
         mine |= 1u << g;
-        lo = fminf(lo, score);
-      } else {
-        hi = fmaxf(hi, score);
+        lo = fminf(lo, score - gtol[g]);
+      } else if (score != -INFINITY) {
+        hi = fmaxf(hi, score + gtol[g]);
       }
     }
     __syncwarp();
@@ -219,8 +223,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 7) route_short_kernel(const 
     if (need_scores) {
       lo = -part_max<L>(-lo);
       hi = part_max<L>(hi);
-      const float tol = p.gtop * (route_tol(p.softmax, smax, lo) + route_tol(p.softmax, smax, hi));
-      const uint32_t near = __ballot_sync(0xffffffffu, valid && hi != -INFINITY && !(lo - hi > tol));
+      const uint32_t near = __ballot_sync(0xffffffffu, valid && hi != -INFINITY && !(lo > hi));
       if (near != 0u) {
         const int lpg = 32 >> (32 - __clz(p.groups - 1));
 #pragma unroll 1

@@ -188,6 +188,34 @@ def test_many_rows(score, E, k, groups, keep, group_top):
             assert int((idx.long() != want).any(1).sum()) == 0, (seed, bias is None)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size,spread", [(30.0, 1e-5), (100.0, 1e-4), (3.0, 1e-6)])
+@pytest.mark.parametrize("T,E,k,groups,keep", [(3000, 16, 4, 8, 4), (12000, 16, 4, 8, 4), (2000, 256, 8, 8, 4),
+                                               (12000, 128, 8, 16, 5)])
+def test_group_scores_whose_keys_cancel(score, size, spread, T, E, k, groups, keep):
+    """A group's two best keys near +size and -size: their sum is far smaller than what their roundings are
+    relative to, and the groups differ by less than those."""
+    g = torch.Generator().manual_seed(E + T)
+    l = torch.randn(T, E, generator=g) * spread
+    gsize = E // groups
+    b = torch.full((groups, gsize), -size)
+    b[:, 0] = size
+    b = b.reshape(E).contiguous()
+    # the groups' scores in fp64: far enough apart that fp64 itself orders them (keys of `size` are rounded by
+    # 2^-53 size each, sums by less)
+    key = oo.scores(l, score) + b.double()
+    rank = key.view(T, groups, gsize).sort(dim=2, descending=True).values[:, :, :2].sum(2)
+    rank = rank.sort(dim=1, descending=True).values
+    clear = rank[:, keep - 1] - rank[:, keep] > 16 * size * 2.0 ** -53
+    assert int(clear.sum()) > 0.99 * T
+    _, idx, _ = _run(l, b, k, "f32", score=score, groups=groups, keep_groups=keep, group_top=2)
+    want = _many_reference(l, b, k, groups, keep, 2, score)
+    # which groups; the order of the experts in them has tests of its own
+    got_groups, want_groups = ((i // gsize).sort(1).values for i in (idx, want))
+    wrong = (got_groups != want_groups).any(1) & clear
+    assert int(wrong.sum()) == 0, f"{int(wrong.sum())} rows with a wrong set of groups"
+
+
 def _special_rows(E, seed):
     """Rows with nothing left, little left, NaN, infinities, ties, saturated and usual logits."""
     l = _logits(26, E, seed)
