@@ -7,7 +7,7 @@
 // and its barriers waited for.  (A block per row with the row in registers leaves
 // the memory idle there: 16384 x 7168 bf16 took 115 us forward against 71 for its
 // bytes.)  A thread has the same columns in all of its rows.  Layer norm of 16384 x 7168
-// bf16: 91 us forward, 124 us backward (5.2 and 5.7 TB/s; a copy reaches 6.6); RMS norm
+// bf16: 91 us forward, 130 us backward (5.2 and 5.4 TB/s; a copy reaches 6.6); RMS norm
 // of 4097 x 5001 fp16: 20 and 43 us.
 //
 // Rows are read and written in 16-byte windows of the memory they lie in: where
@@ -373,8 +373,9 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
     }
     // (a wait that gave up is recorded; the row's results are void)
     mbar_wait(&r.bars[s], phase, &abort_flag, kFaultNormWait);
-    // xh = x rstd - mean rstd
-    const F2 rs = f2(rstd), shift = f2(-mean * rstd);
+    // xh = (x - mean) rstd: the mean first, or (x rstd - mean rstd) rows far from zero
+    // lose the digits that both have in common
+    const F2 rs = f2(rstd), shift = f2(-mean);
     F2 a1 = f2(0.f), a2 = f2(0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
       r.param(0, p.gamma, 1.f, w, m);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const F2 e = f2_mul(d[i], f2_fma(v[i], rs, shift));
+        const F2 e = f2_mul(d[i], f2_mul(f2_add(v[i], shift), rs));
         dg[w][i] = f2_add(dg[w][i], e);
         db[w][i] = f2_add(db[w][i], d[i]);
         a1 = f2_fma(d[i], m[i], a1);
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
     }
     float e1 = 0.f, e2 = 0.f;
     if (!ALIGNED && r.edge >= 0) {
-      const float e = de * fmaf(xe, rstd, -mean * rstd);
+      const float e = de * ((xe - mean) * rstd);
       dg_e += e;
       db_e += de;
       e1 = de * gamma_e;
@@ -409,11 +410,11 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
       const long long ahead = t + static_cast<long long>(p.stages - 1) * p.walkers;
       if (ahead < p.T) r.issue(ahead, s == 0 ? p.stages - 1 : s - 1);
     }
-    // dx = rstd (dy gamma - s1 - xh s2) = (rstd gamma) dy + k1 x + k0
+    // dx = rstd (dy gamma - s1 - xh s2) = (rstd gamma) dy + k1 (x - mean) + k0
     const float s1 = p.rms ? 0.f : sums.x * p.inv_h, s2 = sums.y * p.inv_h;
-    const float k1e = -rstd * rstd * s2, k0e = -rstd * fmaf(s2, -mean * rstd, s1);
+    const float k1e = -rstd * rstd * s2, k0e = -rstd * s1;
     const F2 k1 = f2(k1e), k0 = f2(k0e);
-    if (!ALIGNED && r.edge >= 0) out[r.edge - r.col0] = op_from<T>(fmaf(de, gamma_e * rstd, fmaf(xe, k1e, k0e)));
+    if (!ALIGNED && r.edge >= 0) out[r.edge - r.col0] = op_from<T>(fmaf(de, gamma_e * rstd, fmaf(xe - mean, k1e, k0e)));
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       if (!r.has(w)) continue;
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS, 1) norm_backward_kernel(cons
       r.load(x + r.op_b, w, d);
       r.param(0, p.gamma, 1.f, w, m);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) d[i] = f2_fma(d[i], f2_mul(m[i], rs), f2_fma(v[i], k1, k0));
+      for (int i = 0; i < NP; ++i) d[i] = f2_fma(d[i], f2_mul(m[i], rs), f2_fma(f2_add(v[i], shift), k1, k0));
       r.store(out, w, d);
     }
     if (p.stages == 1) {

@@ -165,6 +165,36 @@ def test_norm_backward_deterministic():
         assert all(torch.equal(p, q) for p, q in zip(a, res[0]))
 
 
+@pytest.mark.parametrize("offset", [10.0, 100.0, 1000.0])
+@pytest.mark.parametrize("T,H", [(3, 96), (40, 1024), (700, 1536), (5, 1001), (700, 515)])
+def test_norm_backward_of_rows_far_from_zero(T, H, offset):
+    """fp32 rows whose mean is far above their spread: the mean is subtracted first, and no error grows with it."""
+    x, gamma, _, dy = _data(T, H, "f32", H, offset)
+    _, m, r = oo.norm(x, None, None, 1e-6, "layer")
+    m, r = m.float(), r.float()
+    r64 = r.double()[:, None]
+    xh = (x.double() - m.double()[:, None]) * r64
+    dy = (dy.double() * 0.3 + xh).float()  # along the rows: the sum of g xh counts in dx
+    d = moe.norm_desc(T, H, "layer", 1e-6, "f32")
+    dx, dgamma, dbeta = torch.empty(T, H, device="cuda"), torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    ws = workspace(moe.moe_norm_backward_workspace_size(d))
+    args = [t.cuda() for t in (dy, x, gamma, m, r)]
+    assert moe.moe_norm_backward(d, *args, dx, dgamma, dbeta, ws) == moe.MOE_OK
+    assert moe.moe_device_error() == (moe.MOE_OK, 0)
+    wdx, wdg, wdb = oo.norm_backward(dy, x, gamma, m, r, "layer")
+    # from the given mean and rstd: a difference, a product, each off by 2^-24 of itself (twice that allowed)
+    xh = xh.abs()
+    dxh = 2.0 ** -22 * xh
+    gg = (dy.double() * gamma.double()).abs()
+    s1, s2 = gg.mean(1, keepdim=True), (gg * xh).mean(1, keepdim=True)
+    e2 = A * s2 + (gg * dxh).mean(1, keepdim=True)
+    tol = r64 * (2.0 ** -22 * (gg + s1 + xh * s2) + A * s1 + xh * e2 + dxh * s2) + wdx.abs() * HALF["f32"] + TINY["f32"]
+    within(dx, wdx, tol, f"dx {T}x{H}")
+    steps = (T / 148 + 64) * 2.0 ** -24
+    within(dgamma, wdg, (dy.double().abs() * (steps * xh + dxh)).sum(0) + 1e-37, "dgamma")
+    within(dbeta, wdb, steps * dy.double().abs().sum(0) + 1e-37, "dbeta")
+
+
 def test_norm_offsets_past_32_bits():
     T, H = 160_000, 16384  # 5.2 GB of bf16
     x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(0.1, 1.0)
