@@ -195,6 +195,30 @@ def test_norm_backward_of_rows_far_from_zero(T, H, offset):
     within(dbeta, wdb, steps * dy.double().abs().sum(0) + 1e-37, "dbeta")
 
 
+# Many rows a group: rings that wrap, several groups a block, block counts cut to whole windows, parameters in
+# shared memory; odd rows, whole windows and the longest ones.
+MANY = [(4097, 5001), (3001, 257), (5000, 33), (149, 1031), (296, 4100), (700, 8193), (700, 16383), (5000, 64), (1200, 2048),
+        (1500, 7168), (450, 16384)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("T,H", MANY)
+def test_norm_many_rows(dtype, kind, T, H):
+    x, gamma, beta, _ = _data(T, H, dtype, T + 3 * H)
+    _check(x, gamma, beta if kind == "layer" else None, dtype, kind)
+    _check(x, gamma, None, dtype, kind, inplace=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("T,H", MANY)
+def test_norm_backward_many_rows(dtype, kind, T, H):
+    x, gamma, _, dy = _data(T, H, dtype, 5 * T + H)
+    _check_backward(x, dy, gamma, dtype, kind)
+    _check_backward(x, dy, gamma, dtype, kind, need=(True, False), alias="x" if kind == "layer" else "dy")
+
+
 def test_norm_offsets_past_32_bits():
     T, H = 160_000, 16384  # 5.2 GB of bf16
     x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(0.1, 1.0)
