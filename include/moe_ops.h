@@ -176,12 +176,13 @@ typedef struct {
 /* norm = sqrt(sum of g^2) or max |g| over all elements of all tensors (the host
  * array `list`, 0 <= count <= 65536), norm_out[0] = norm (fp32, device), and
  *   out = g * min(1, max_norm / (norm + 1e-6)),
- * rounded once to each tensor's type.  max_norm: finite, >= 0.  Squares are added
- * up so that neither large nor small fp32 values overflow or vanish, in fp64 and a
- * fixed order.  Where the norm is not finite (a gradient is inf or NaN) nothing is
- * scaled: out = g, and the caller sees it in norm_out.  `list` is read during the
- * call only.  Workspace: moe_clip_grads_workspace_size(list, count) bytes (0 for a
- * bad list). */
+ * the factor in fp32 and the product rounded once to each tensor's type.  max_norm:
+ * finite, >= 0.  Squares are added up in a fixed order and so that neither large nor
+ * small fp32 values overflow or vanish: the 4 or 8 of 16 bytes in fp32 where it holds
+ * them, else in fp64, and these sums in fp64.  Where norm_out is not finite (a gradient
+ * is inf or NaN, or the norm is beyond the largest fp32 number) nothing is scaled:
+ * out = g.  `list` is read during the call only.
+ * Workspace: moe_clip_grads_workspace_size(list, count) bytes (0 for a bad list). */
 MOE_API size_t moe_clip_grads_workspace_size(const moe_grad_tensor* list, int32_t count);
 MOE_API moe_status moe_clip_grads(const moe_grad_tensor* list, int32_t count, moe_clip_norm kind, float max_norm,
                                   float* norm_out, void* ws, size_t ws_bytes, moe_stream_t stream);

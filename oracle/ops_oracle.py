@@ -152,12 +152,14 @@ def linear_backward(dy, pre, x, weight, kind):
 
 # ------------------------------------------------------------------------------ clipping
 def clip(grads, max_norm, kind="l2"):
-    """(norm, [g * factor])"""
+    """(norm, [g * factor]); a norm past fp32 is infinite, and nothing is scaled"""
     gs = [g.to(F64).reshape(-1) for g in grads]
     flat = torch.cat(gs) if gs else torch.zeros(0, dtype=F64)
     if kind == "l2":
         norm = float(flat.pow(2).sum().sqrt())
     else:
         norm = float("nan") if torch.isnan(flat).any() else float(flat.abs().max()) if flat.numel() else 0.0
-    c = min(1.0, max_norm / (norm + 1e-6)) if math.isfinite(norm) else 1.0
+    if not math.isfinite(float(torch.tensor(norm, dtype=F64).to(torch.float32))):
+        return (norm if math.isnan(norm) else INF), gs
+    c = min(1.0, max_norm / (norm + 1e-6))
     return norm, [g * c for g in gs]

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(CLIP_THREADS)
 }
 
 template <typename T>
-__device__ __forceinline__ void clip_scale_chunk(const void* p, void* out, long long n, long long v0, int nv, float coef) {
+__device__ __forceinline__ void clip_scale_chunk(const void* p, void* out, long long n, long long v0, int nv, float2 coef) {
   T* o = static_cast<T*>(out);
   // one alignment for both: whole vectors are written as such
   const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0u;
@@ -211,7 +211,7 @@ __device__ __forceinline__ void clip_scale_chunk(const void* p, void* out, long 
     constexpr int W = decltype(vl)::value;
     float g[W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) g[j] = f[j] * coef;
+    for (int j = 0; j < W; ++j) g[j] = (f[j] * coef.x) * coef.y;
     if (W > 1 && same) {
       if constexpr (W > 1) *reinterpret_cast<uint4*>(o + at) = op_pack16<T>(g);
     } else {
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(CLIP_THREADS)
     clip_scale_kernel(const __grid_constant__ ClipList<MAXT> l, const double* __restrict__ partial, int parts,
                       float max_norm, float* __restrict__ norm_out) {
   __shared__ double red[CLIP_THREADS / 32];
-  __shared__ float s_coef;
+  __shared__ float2 s_coef;
   pdl_next();
   pdl_wait();
   // every block forms the same norm, in the same order
@@ -251,17 +251,23 @@ __global__ void __launch_bounds__(CLIP_THREADS)
       else a += red[w];
     }
     const double norm = MAX ? a : sqrt(a);
+    const float norm32 = static_cast<float>(norm);
     const double coef = static_cast<double>(max_norm) / (norm + 1e-6);
-    // not below 1, or no number: nothing is scaled
-    s_coef = isfinite(norm) && coef < 1.0 ? static_cast<float>(coef) : 1.0f;
-    if (norm_out != nullptr && blockIdx.x == 0) *norm_out = static_cast<float>(norm);
+    // not below 1, or a norm that is no fp32 number: nothing is scaled.  A factor below
+    // the smallest normal number (gradients near the largest ones) goes in two steps,
+    // the second of them 2^-64, or its digits would be lost.
+    const bool small = coef < 0x1p-126;
+    s_coef = isfinite(norm32) && coef < 1.0
+                 ? make_float2(static_cast<float>(small ? coef * 0x1p64 : coef), small ? 0x1p-64f : 1.0f)
+                 : make_float2(1.0f, 1.0f);
+    if (norm_out != nullptr && blockIdx.x == 0) *norm_out = norm32;
   }
   __syncthreads();
-  const float coef = s_coef;
+  const float2 coef = s_coef;
   ClipCursor<MAXT> cur(l);
   for (int c = l.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
     cur.seek(c);
-    if (coef == 1.0f && cur.in == cur.out) continue;
+    if (coef.x == 1.0f && cur.in == cur.out) continue;
     const long long v0 = static_cast<long long>(c - cur.lo) * l.chunk;
     if (cur.type == kClipF32)
       clip_scale_chunk<float>(cur.in, cur.out, cur.n, v0, l.chunk, coef);

@@ -102,6 +102,30 @@ def test_squares_beyond_fp32(value):
         _check(g, 1.0, "max")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [1e30, 1e-30, 3e38, 1e-38])
+@pytest.mark.parametrize("max_norm", [1.0, 1e-3, 0.0])
+def test_factors_of_any_size(value, max_norm, dtype):
+    """Factors below the smallest normal fp32 number lose nothing; a norm past the largest one is not finite."""
+    for count in (1, 1000):
+        g = [torch.full((count,), value, dtype=DT[dtype], device="cuda"), torch.zeros(50, dtype=DT[dtype], device="cuda")]
+        for kind in ("l2", "max"):
+            _check([t.clone() for t in g], max_norm, kind)
+
+
+def test_a_norm_past_fp32_leaves_the_gradients():
+    """Finite gradients whose norm fp32 does not hold: norm_out is not finite, so nothing is scaled."""
+    g = [torch.full((1000,), 3e38, device="cuda"), torch.full((7,), 2.0, dtype=torch.bfloat16, device="cuda")]
+    keep = [t.clone() for t in g]
+    assert _run(g, None, 1.0) == math.inf
+    for a, b in zip(g, keep):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    out = [torch.zeros_like(t) for t in g]
+    assert _run(g, out, 1.0) == math.inf
+    for a, b in zip(out, keep):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("kind", ["l2", "max"])
 def test_non_finite_gradients_are_reported_and_left(bad, kind):

@@ -123,6 +123,28 @@ def test_activations_far_out(act, dtype):
     within(db, want, 2.0 ** -18 * torch.ones_like(want) * (1.0 + p1[0].double().abs().clamp_max(10.0)), act + "'")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_keep_small_values(act, dtype):
+    """fp32 outputs of activations far on the negative side, where they are small: relative errors."""
+    v = torch.cat([torch.linspace(-9, 9, 577), torch.linspace(-12.5, -9, 63)]).to(DT[dtype])
+    v = v[v != 0]
+    for rows, cols in ((32, 64), (2600, 1024)):  # a few rows, and enough for the wide tiles
+        g = torch.Generator().manual_seed(rows)
+        x = torch.zeros(rows, 64, dtype=DT[dtype])
+        at = torch.randint(0, v.numel(), (rows, 64), generator=g)
+        x[:] = v[at]
+        w = torch.zeros(cols, 64, dtype=DT[dtype])
+        w[:64] = torch.eye(64).to(DT[dtype])
+        y = torch.empty(rows, cols, device="cuda")
+        assert _linear(moe.linear_desc(rows, cols, 64, act, dtype, "f32"), x.cuda(), w.cuda(), None, None, None, y) == moe.MOE_OK
+        a = x.double()
+        want = {"silu": lambda: a * torch.sigmoid(a), "gelu": lambda: 0.5 * a * torch.erfc(-a / math.sqrt(2.0)),
+                "gelu_tanh": lambda: a * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3))}[act]()
+        arg = {"silu": a.abs(), "gelu": a * a / 2, "gelu_tanh": 2 * math.sqrt(2 / math.pi) * (a.abs() + 0.044715 * a.abs() ** 3)}[act]
+        within(y[:, :64], want, want.abs() * (2.0 ** -19 + 2.0 ** -21 * arg) + 2.0 ** -126, act)
+
+
 def _check_backward(M, N, K, dtype, act, need=(True, True, True)):
     x, w, b, dy = _data(M, N, K, dtype, M + N + 7 * K)
     dy = dy.to(DT[dtype])
