@@ -136,7 +136,9 @@ typedef struct {
 /* y = act(x[M, K] . W[N, K]^T + bias) + residual, on the tensor cores with fp32
  * accumulation; bias, activation and residual are applied to the fp32
  * accumulator and y is rounded once.  (Activations by fast exponentials and
- * reciprocals, erf to 1.5e-7: within 2^-18 of their value and 2^-19 of |a|.)
+ * reciprocals: a relative error of at most 2^-19 + 2^-21 z, z the exponent's size: |a|,
+ * a^2 / 2 or 2 sqrt(2 / pi) (|a| + 0.044715 |a|^3); sigmoids and exponentials below
+ * 2^-126 count as 0.)
  * bias [N] fp32, residual [M, N] in the type
  * of y, each NULL for none; pre [M, N] in `dtype` receives x W^T + bias for the
  * backward pass, or is NULL.  y may be the residual.  N or K not a multiple of 8
