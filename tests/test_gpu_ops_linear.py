@@ -250,3 +250,37 @@ def test_deterministic():
             assert _linear(moe.linear_desc(M, 2048, 2048, "gelu"), x, w, b, res, None, y) == moe.MOE_OK
             outs.append(y.cpu())
         assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements of y, pre, dy and dp: the last rows and columns come out as the formulas give them."""
+    M, N, K = 66000, 66048, 64
+    x, w, b, _ = _data(M, 64, K, "bf16", 1)
+    w = (torch.randn(N, K, device="cuda") * K ** -0.5).bfloat16()
+    b = torch.randn(N, device="cuda") * 0.2
+    d = moe.linear_desc(M, N, K, "silu")
+    y, pre = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert _linear(d, x, w, b, None, pre, y) == moe.MOE_OK
+    rows, cols = slice(M - 5, M), slice(N - 72, N)
+    want_pre, want = oo.linear(x[rows], w[cols], b[cols], None, "silu")
+    err = _accumulation(K) * (x[rows].double().abs() @ w[cols].double().abs().T) + 2.0 ** -23 * want_pre.abs()
+    within(pre[rows, cols], want_pre.cpu(), (err + want_pre.abs() * HALF["bf16"] + TINY["bf16"]).cpu(), "pre")
+    tol = 1.13 * err + 2.0 ** -19 * (want_pre.abs() + 1.0) + want.abs() * (HALF["bf16"] + 2.0 ** -23) + TINY["bf16"]
+    within(y[rows, cols], want.cpu(), tol.cpu(), "y")
+    # gradients: dy is y; the last row of dx, and the last rows of dW by all of dp
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    ws = workspace(moe.moe_linear_backward_workspace_size(d))
+    assert moe.moe_linear_backward(d, y, pre, x, w, dx, dw, db, ws) == moe.MOE_OK
+    assert moe.moe_device_error() == (moe.MOE_OK, 0)
+    last = slice(M - 1, M)
+    _, wdx, _, _ = oo.linear_backward(y[last], pre[last], x[last], w, "silu")
+    dp = (y[last].double() * oo.act_grad(pre[last], "silu")).abs()
+    edp = 2.0 ** -19 * y[last].double().abs() * (1.0 + pre[last].double().abs()) + dp * HALF["bf16"] + TINY["bf16"]
+    tol = (edp + _accumulation(N) * dp) @ w.double().abs() + wdx.abs() * HALF["bf16"] + TINY["bf16"]
+    within(dx[last], wdx.cpu(), tol.cpu(), "dx")
+    _, _, wdw, wdb = oo.linear_backward(y[:, cols].contiguous(), pre[:, cols].contiguous(), x, w[cols], "silu")
+    dp = (y[:, cols].double() * oo.act_grad(pre[:, cols], "silu")).abs()
+    ev = 2.0 ** -19 * y[:, cols].double().abs() * (1.0 + pre[:, cols].double().abs())
+    tol = (ev + dp * HALF["bf16"] + TINY["bf16"] + _accumulation(M) * dp).T @ x.double().abs() + wdw.abs() * HALF["bf16"] + TINY["bf16"]
+    within(dw[cols], wdw.cpu(), tol.cpu(), "dweight")
+    within(db[cols], wdb.cpu(), ((M / 148 + 64) * 2.0 ** -24 * dp.sum(0) + ev.sum(0) + 1e-37).cpu(), "dbias")
