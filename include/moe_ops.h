@@ -62,7 +62,9 @@ typedef struct {
  * one; a group with no unmasked expert comes after every other.  Where fewer
  * than k unmasked experts remain, masked ones of the kept groups follow in
  * ascending order with weight 0; where all the chosen ones are masked, the
- * weights are 0.  A row's k indices are always distinct and in [0, E), as
+ * weights are 0.  An expert whose bias is -inf or NaN is ordered as a masked one,
+ * but keeps the weight of its score.  (A sigmoid score below 2^-126 counts as 0
+ * beside chosen ones whose sum is above 1e-18: a share of less than 1e-20.)  A row's k indices are always distinct and in [0, E), as
  * moe_permute needs them.  A +inf logit is the limit of large ones.
  * idx [T, k] int32, w [T, k] fp32. */
 MOE_API moe_status moe_route(const moe_route_desc* d, const void* logits, const float* bias, int32_t* idx, float* w,
@@ -151,7 +153,10 @@ MOE_API moe_status moe_linear(const moe_linear_desc* d, const void* x, const voi
 
 /* With dp = dy act'(pre) (pre from moe_linear; NULL for MOE_ACT_NONE):
  *   dx = dp . W [M, K],  dweight = dp^T . x [N, K],  dbias = sum_m dp [N] fp32
- * dp is rounded once to `dtype` as the products' operand; dbias is summed from the
+ * dp is rounded once to `dtype` as the products' operand, where there is an
+ * activation (with it the gradients carry two roundings: about 1.4 times the error
+ * that the rounding of dx and dweight alone leaves; and MOE_F16 loses dp below 2^-25, so
+ * the loss has to be scaled, as it has for dy itself); dbias is summed from the
  * unrounded fp32 dp in a fixed order.  dx, dweight and dbias may each be NULL; dx
  * and dweight are in `dtype`, dy [M, N] in `dtype`.  relu'(0) = 0.  The residual's
  * gradient is dy itself.  M = 0 writes zeros to dweight and dbias.

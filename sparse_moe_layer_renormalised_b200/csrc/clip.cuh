@@ -6,8 +6,8 @@
 // and so looks at few entries of the list, which is slow to index; in the second
 // chunks are dealt out in turn, which the writes prefer (for 322M fp32 gradients
 // 205 against 238 us in the first pass, 445 against 490 in the second).  Whole vectors
-// go without bounds, a chunk's last round with all of its loads at once.  Together 642 us
-// for the 322M gradients in 393 tensors: 217 (5.9 TB/s) and 425 (6.1).
+// go without bounds, a chunk's last round with all of its loads at once.  Together 613 to
+// 651 us for the 322M gradients in 393 tensors, about a third and two thirds (5.9 to 6.3 TB/s).
 //
 // The tensor list travels in the kernel's parameters (at most CLIP_MAX tensors
 // a launch), so a captured graph holds it and nothing has to be copied.

@@ -855,7 +855,9 @@ __global__ void __launch_bounds__(LS_THREADS, 2)
 }
 
 // ------------------------------------------------------------------------------ dp and dbias
-// dp = dy act'(pre), rounded to the operand type (skipped where dp is null), and
+// dp = dy act'(pre), rounded to the operand type (skipped where dp is null): the tensor
+// cores take 16-bit operands, and a second product over what the rounding cut off would
+// double the gradients' time for an error of 1.7e-3 instead of 2.3e-3 (bf16); and
 // each block's column sums of the unrounded dp (skipped where part is null):
 // part[blockIdx.y][N].  Thread = 8 columns; a block walks over `rows` rows from
 // blockIdx.y * rows on.

@@ -7,8 +7,9 @@
 // and its barriers waited for.  (A block per row with the row in registers leaves
 // the memory idle there: 16384 x 7168 bf16 took 115 us forward against 71 for its
 // bytes.)  A thread has the same columns in all of its rows.  Layer norm of 16384 x 7168
-// bf16: 91 us forward, 130 us backward (5.2 and 5.4 TB/s; a copy reaches 6.6); RMS norm
-// of 4097 x 5001 fp16: 20 and 43 us.
+// bf16: 92 us forward, 130 us backward, 138 in a long run of calls (5.1 and 5.4 TB/s; a copy
+// reaches 6.6); RMS norm of 4097 x 5001 fp16: 21 and 50 us out of memory, 18 and 44 where a
+// part is still in L2.
 //
 // Rows are read and written in 16-byte windows of the memory they lie in: where
 // the row length is no multiple of a window, row t starts `a` elements into one,

@@ -337,8 +337,9 @@ LinWidePlan lin_wide_plan(long long Q, long long P, int nkb, int pairs) {
 // Bytes for the partial sums of a last wave, whatever the plan: one tile a pair.
 size_t lin_wide_ws() { return static_cast<size_t>(op_sms() / 2) * 256 * 256 * 4; }
 
-// The skinny kernel for few rows (bf16, skinny against wide: 32 x 7168 x 3584 13.4 and 22.7
-// us, 128 rows 17.0 and 23.5, 160 rows 22.5 and 23.8, 512 rows 36 and 28.6), and for
+// The skinny kernel for few rows, one tile of them (bf16, skinny against wide: 32 x 7168 x
+// 3584 13.4 and 22.7 us, 128 rows 17.0 and 23.5; two tiles fetch the weights twice: 160 rows
+// 22.5 and 23.8, which is not worth a rule of its own, and 512 rows 36 and 28.6), and for
 // outputs whose 128 x 128 tiles take half of the SMs at most: it splits their sums
 // over several CTAs (1024 x 896 x 7168 20.7 and 22.5, 1024 x 1024 x 1024 10.6 and 13.3; 1024
 // x 2048 x 2048, 128 tiles, 23.4 and 20.4).

@@ -2,8 +2,10 @@
 // top-k in the exact order of the keys, weights; and the weights' gradient.
 //
 // Forward: one warp per token, its row of at most 1024 logits in registers.  (Many
-// short rows: route_short.cuh.)  What bounds it is instruction issue next to the one
-// read of the logits (16384 x 896 fp32, sigmoid + bias, top 16: 27 us, 59 MB in 9), so
+// short rows: route_short.cuh.)  What it costs are the instructions next to the one read
+// of the logits (16384 x 896 fp32, sigmoid + bias, top 16: 27 us, 59 MB in 9; 59 % of the
+// issue slots taken) and the waits of a token's one chain of steps, which the 32 warps
+// of an SM that the registers allow do not cover.  So
 // the top-k does not run k arg-max rounds over all keys: the k-th largest of
 // the 32 lanes' own maxima (one 32-wide sort) is a lower bound of the k-th key,
 // and only the few keys at or above it (22 of 896 at k = 16, on average) are
@@ -91,10 +93,11 @@ __device__ __forceinline__ float route_score(float l, int softmax, float m, floa
   return 1.0f / (1.0f + expf(-l));
 }
 
-// Share of each lane's chosen logit (-inf: none) in the sum of the chosen scores,
-// free of underflow: softmax scores relative to the largest chosen one; sigmoid
-// scores as they are, or, where all are below 1e-18, as e^l (sigmoid(l) = e^l up
-// to a relative e^l) relative to the largest.  0 everywhere where all are masked.
+// Share of each lane's chosen logit (-inf: none) in the sum of the chosen scores;
+// what underflows is a share below 1e-20: softmax scores relative to the largest
+// chosen one; sigmoid scores as they are, or, where all are below 1e-18, as e^l
+// (sigmoid(l) = e^l up to a relative e^l) relative to the largest.  0 everywhere
+// where all are masked.
 __device__ __forceinline__ float route_share(float l, int softmax) {
   float s = 0.f, total = 0.f;
   if (!softmax) {
@@ -582,7 +585,10 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, 8) route_kernel(const RouteP
 // Gradient of the weights.  One warp per token.  Sigmoid scores and renormalised
 // softmax scores reach the chosen logits only (the row is cleared and k values
 // are put in); plain softmax scores reach every logit, and the row is read once,
-// into registers.  Bound by the write of dlogits (and that read).
+// into registers.  16384 x 896 bf16, the first form 12 to 13 us, bound by the start of
+// so many warps and the loads they wait for (40 % of the issue slots), the plain
+// softmax 17 us, 21 out of memory: the exponentials of a whole row, 64 % of the issue
+// slots with 29 of 64 warps.
 template <typename T, int VL, int CH>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32, 8)
     route_backward_kernel(const RouteParams p, const int32_t* __restrict__ idx, const float* __restrict__ dw,
