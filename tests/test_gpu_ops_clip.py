@@ -87,6 +87,14 @@ def test_many_tensors(count):
     _check(_grads(sizes, ["f32", "bf16"], count), 0.7)
 
 
+def test_the_most_tensors():
+    buf = torch.randn(65536 * 5, generator=torch.Generator().manual_seed(2)).cuda()
+    want_norm, (want,) = oo.clip([buf.cpu()], 1.0)
+    norm = _run(list(buf.split(5)), None, 1.0)
+    assert abs(norm - want_norm) <= 1e-6 * want_norm
+    within(buf, want, want.abs() * 2.0 ** -20)
+
+
 @pytest.mark.parametrize("value", [1e30, 1e-30, 3e38, 1e-38])
 def test_squares_beyond_fp32(value):
     """Squares that overflow or vanish in fp32 (and in bf16's range) are added up in fp64."""

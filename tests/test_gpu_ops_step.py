@@ -188,6 +188,53 @@ def test_two_streams_at_once():
     assert moe.moe_device_error() == (moe.MOE_OK, 0)
 
 
+def test_streams_that_fork_and_join_captured_and_not():
+    """A step over two streams that wait for one another several times, as it is and as a captured graph: the
+    same bits as on one stream."""
+    T, H, E, bf = 700, 1536, 256, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    randn = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, W, Wr = randn(T, H).to(bf), (randn(H, H) * H ** -0.5).to(bf), (randn(E, H) * H ** -0.5).to(bf)
+    nd, ld, lr = moe.norm_desc(T, H, "rms"), moe.linear_desc(T, H, H, "silu"), moe.linear_desc(T, E, H, "none", "bf16", "f32")
+    rd = moe.route_desc(T, E, 8, groups=8, keep_groups=4, group_top=2)
+    xn, a, b, ca, cb = (torch.empty(T, H, dtype=bf, device="cuda") for _ in range(5))
+    logits, idx, w = torch.empty(T, E, device="cuda"), torch.empty(T, 8, dtype=torch.int32, device="cuda"), torch.empty(T, 8, device="cuda")
+    norm, grads = torch.empty(1, device="cuda"), moe.tensor_list([a, b], [ca, cb])
+    size = max(moe.moe_linear_workspace_size(ld), moe.moe_linear_workspace_size(lr))
+    ws1, ws2, cws = workspace(size), workspace(size), workspace(moe.moe_clip_grads_workspace_size(grads))
+
+    def step(side):
+        main, c, cur = torch.cuda.current_stream(), moe.check, x
+        for _ in range(6):
+            c(moe.moe_norm(nd, cur, None, None, xn))
+            side.wait_stream(main)
+            c(moe.moe_linear(ld, xn, W, None, None, None, a, ws1))
+            with torch.cuda.stream(side):
+                c(moe.moe_linear(lr, xn, Wr, None, None, None, logits, ws2))
+                c(moe.moe_route(rd, logits, None, idx, w))
+                c(moe.moe_linear(ld, xn, W, None, xn, None, b, ws2))
+            main.wait_stream(side)
+            c(moe.moe_clip_grads(grads, "l2", 100.0, norm, cws))
+            cur = cb
+
+    results = lambda: [t.clone() for t in (a, b, ca, cb, logits, idx, w, norm)]  # noqa: E731
+    step(torch.cuda.current_stream())
+    want = results()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(torch.cuda.Stream())
+    for run in (lambda: step(side), graph.replay):
+        for _ in range(4):
+            for t in (xn, a, b, ca, cb, logits):
+                t.fill_(float("nan"))
+            run()
+            torch.cuda.synchronize()
+            for p, q in zip(results(), want):
+                assert torch.equal(p, q)
+    assert moe.moe_device_error() == (moe.MOE_OK, 0)
+
+
 def test_calls_after_one_another_without_waiting():
     """Many calls in a row on one stream, outputs of one the inputs of the next, as
     launches that overlap would break them."""
