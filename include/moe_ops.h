@@ -64,8 +64,9 @@ typedef struct {
  * ascending order with weight 0; where all the chosen ones are masked, the
  * weights are 0.  An expert whose bias is -inf or NaN is ordered as a masked one,
  * but keeps the weight of its score.  (A sigmoid score below 2^-126 counts as 0
- * beside chosen ones whose sum is above 1e-18: a share of less than 1e-20.)  A row's k indices are always distinct and in [0, E), as
- * moe_permute needs them.  A +inf logit is the limit of large ones.
+ * beside chosen ones whose sum is above 1e-18: a share of less than 1e-20.)
+ * A row's k indices are always distinct and in [0, E), as moe_permute needs them.
+ * A +inf logit is the limit of large ones.
  * idx [T, k] int32, w [T, k] fp32. */
 MOE_API moe_status moe_route(const moe_route_desc* d, const void* logits, const float* bias, int32_t* idx, float* w,
                              moe_stream_t stream);

@@ -80,8 +80,8 @@ constexpr float kSqrt2OverPi = 0.7978845608028654f;
 
 // erfc(x) = e^(-x^2) t P(t), t = 1 / (1 + 0.375 x), at x = |a| / sqrt 2, with a polynomial
 // fitted for the least relative error over 0 <= x <= 9.5 (weighted least squares,
-// the weights moved to the largest errors until these were level): 6.4e-7.  Half of
-// erff's instructions, and no branch.  (The bound has to be relative: gelu's values are
+// the weights moved to the largest errors until these were level): 6.4e-7.  Fewer
+// instructions than erff's, and no branch.  (The bound has to be relative: gelu's values are
 // small where a is negative.  Five terms with an absolute error of 1.5e-7 are off by 5e-4
 // of the value at a = -4.)
 constexpr float kErfcX = 0.375f * 0.7071067811865476f;

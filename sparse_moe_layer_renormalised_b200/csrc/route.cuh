@@ -5,13 +5,12 @@
 // short rows: route_short.cuh.)  What it costs are the instructions next to the one read
 // of the logits (16384 x 896 fp32, sigmoid + bias, top 16: 27 us, 59 MB in 9; 59 % of the
 // issue slots taken) and the waits of a token's one chain of steps, which the 32 warps
-// of an SM that the registers allow do not cover.  So
-// the top-k does not run k arg-max rounds over all keys: the k-th largest of
-// the 32 lanes' own maxima (one 32-wide sort) is a lower bound of the k-th key,
-// and only the few keys at or above it (22 of 896 at k = 16, on average) are
-// listed and sorted, 32 at a time.  For the same reason sigmoid + bias keys are
-// first formed with one hardware tanh each, to 2.6e-4, and exactly enough to be
-// sorted for the candidates alone.
+// of an SM that the registers allow do not cover.  So the top-k does not run k arg-max
+// rounds over all keys: the k-th largest of the 32 lanes' own maxima is a lower bound
+// of the k-th key, and only the few keys at or above it (22 of 896 at k = 16, on
+// average) are listed and sorted, 32 at a time.  For the same reason sigmoid + bias
+// keys are first formed with one hardware tanh each, to 2.6e-4, and exactly enough to
+// be sorted for the candidates alone.
 //
 // Exact order from fp32 arithmetic: the fp32 keys carry an error of at most
 // route_tol; where two neighbours in the sorted list (or the last chosen and
